@@ -173,6 +173,52 @@ ss_status ss_dense_gemm(const void *Xq, const float *s_x, const void *Wq, const 
                         int64_t M, int64_t N, int64_t K_p, ss_qdtype q, void *Y,
                         ss_out_dtype out_dtype, ss_stream_t stream);
 
+/* What a fused GEMM does to an output before its one rounding to Y's type
+ * (bias, activation and residual of a transformer's projections), all in
+ * fp32 on v[m, n] = the plain call's fp32 value + bias[n]:
+ *   plain:  Y[m, n]         = act(v[m, n]) + residual[m, n]     Y is [M, N]
+ *   gated:  Y[m, 8 g + i]   = act(v[m, 16 g + i]) * v[m, 16 g + 8 + i],
+ *           i = 0..7                                            Y is [M, N/2]
+ * A gated weight (and bias) holds its rows in groups of 16: eight gate rows,
+ * then the eight rows they multiply; arrange them before the weight is
+ * compressed.  act:
+ *   SS_ACT_NONE      v                     SS_ACT_RELU  max(v, 0), NaN stays
+ *   SS_ACT_SILU      v / (1 + e^-v)
+ *   SS_ACT_GELU      v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2
+ *   SS_ACT_GELU_ERF  v (1 + erf(v / sqrt 2)) / 2
+ * bias is [N], residual [M, N] row-major, each NULL or 16-byte aligned, bf16
+ * or fp32 whatever Y's type.  The residual may be Y itself (same type): it is
+ * then updated in place; otherwise Y overlaps no input.  SS_ERR_INVALID_ARG:
+ * an unknown act or dtype, gated not 0 or 1, gated with N not a multiple of
+ * 16.  SS_ERR_UNSUPPORTED: gated with a residual. */
+typedef enum {
+    SS_ACT_NONE = 0,
+    SS_ACT_RELU = 1,
+    SS_ACT_SILU = 2,
+    SS_ACT_GELU = 3,
+    SS_ACT_GELU_ERF = 4
+} ss_act;
+
+typedef struct {
+    const void *bias;
+    const void *residual;
+    ss_in_dtype bias_dtype;
+    ss_in_dtype residual_dtype;
+    ss_act act;
+    int32_t gated;
+} ss_epilogue;
+
+/* ss_sparse_gemm and ss_dense_gemm with the fused epilogue *epi (read during
+ * the call; NULL, or one that does nothing, runs the plain kernels). */
+ss_status ss_sparse_gemm_fused(int sparse_operand, const void *Av, const void *Am,
+                               const float *s_a, const void *B, const float *s_b, int64_t M,
+                               int64_t N, int64_t K_lp, ss_qdtype q, const ss_epilogue *epi,
+                               void *Y, ss_out_dtype out_dtype, ss_stream_t stream);
+ss_status ss_dense_gemm_fused(const void *Xq, const float *s_x, const void *Wq, const float *s_w,
+                              int64_t M, int64_t N, int64_t K_p, ss_qdtype q,
+                              const ss_epilogue *epi, void *Y, ss_out_dtype out_dtype,
+                              ss_stream_t stream);
+
 /* ------------------------------------------------------------------------
  * NVFP4 with pairwise sparsity (the Blackwell sparse FP4 of the "add 2:4 or
  * drop a precision tier?" study, paper-daily 2610.28947, 3.3: 2 of every 4
@@ -253,6 +299,97 @@ ss_status ss_sparse_gemm_nvfp4(const void *Wv, const void *Wm, const void *Ws, c
 ss_status ss_dense_gemm_nvfp4(const void *Xv, const void *Xs, const float *g_x, const void *Wv,
                               const void *Ws, const float *g_w, int64_t M, int64_t N,
                               int64_t K_p, void *Y, ss_out_dtype out_dtype, ss_stream_t stream);
+
+/* The NVFP4 GEMMs with the fused epilogue *epi (see ss_epilogue). */
+ss_status ss_sparse_gemm_nvfp4_fused(const void *Wv, const void *Wm, const void *Ws,
+                                     const float *g_w, const void *Xv, const void *Xs,
+                                     const float *g_x, int64_t M, int64_t N, int64_t K_lp,
+                                     const ss_epilogue *epi, void *Y, ss_out_dtype out_dtype,
+                                     ss_stream_t stream);
+ss_status ss_dense_gemm_nvfp4_fused(const void *Xv, const void *Xs, const float *g_x,
+                                    const void *Wv, const void *Ws, const float *g_w, int64_t M,
+                                    int64_t N, int64_t K_p, const ss_epilogue *epi, void *Y,
+                                    ss_out_dtype out_dtype, ss_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Around the products of a transformer layer.
+ * ------------------------------------------------------------------------ */
+
+/* RMS norm fused into ss_quant_lift_act (the input of the attention and the
+ * feed-forward projections).  Per token m of X[M, K], in fp32:
+ *   y[k] = X[m, k] * rsqrt(mean_k X[m, k]^2 + eps) * weight[k]
+ * then as ss_quant_lift_act on y, which is never written or rounded itself
+ * (SS_BF16: rounded to bf16 as it is stored).  weight is [K], bf16 or fp32
+ * whatever X's type; eps >= 0.  Rows must be finite, with a sum of squares
+ * below the fp32 range; a row with max|y| < 1e-35 has codes 0 and s_x 0. */
+ss_status ss_norm_quant_lift_act(const void *X, ss_in_dtype in_dtype, const void *weight,
+                                 ss_in_dtype weight_dtype, float eps, int64_t M, int64_t K,
+                                 ss_pattern p, ss_qdtype q, void *Xq_lift, float *s_x,
+                                 ss_stream_t stream);
+
+/* Rotary positions of query and key heads, one call for both.  Per token t,
+ * head and pair i < rot_dim / 2, with c, s = cos, sin of
+ * positions[t] * freqs[i] (formed in 64 bits):
+ *   a' = scale (a c - b s),  b' = scale (b c + a s)      in fp32, rounded once
+ * where (a, b) are elements (i, i + rot_dim/2) of the head (SS_ROPE_HALF) or
+ * (2i, 2i + 1) (SS_ROPE_INTERLEAVED).  Elements from rot_dim on are copied.
+ * Negated positions turn back: with them the call maps the gradient of the
+ * output to that of the input.
+ *
+ * A ss_rope_heads describes [T, heads, head_dim] heads with unit element
+ * stride and any token and head strides (in elements), so the heads may lie
+ * inside a fused projection's output.  out may be in, with the same strides
+ * (rotated in place); otherwise the outputs overlap no input and one another
+ * nowhere.  Pointers need only the element's alignment; 16-byte aligned rows
+ * run faster.  k may be NULL.  positions: int32, or int64 if positions64 = 1
+ * (any sign, |position| < 2^53).  freqs: [rot_dim / 2] doubles in device
+ * memory.  T in [1, 2^31 - 8), heads in [1, 65536], rot_dim even and at most
+ * head_dim; SS_ERR_UNSUPPORTED for head_dim > 1024. */
+typedef enum { SS_ROPE_HALF = 0, SS_ROPE_INTERLEAVED = 1 } ss_rope_layout;
+
+typedef struct {
+    const void *in;
+    void *out;
+    int64_t heads;
+    int64_t in_token, in_head;   /* strides in elements */
+    int64_t out_token, out_head;
+} ss_rope_heads;
+
+ss_status ss_rope(const ss_rope_heads *q, const ss_rope_heads *k, ss_in_dtype dtype,
+                  const void *positions, int32_t positions64, const double *freqs, float scale,
+                  int64_t T, int64_t head_dim, int64_t rot_dim, ss_rope_layout layout,
+                  ss_stream_t stream);
+
+/* The frequencies and the scale that ss_rope takes, written to HOST memory:
+ * freqs[i] = base^(-2i/rot_dim), i < rot_dim / 2, stretched for contexts past
+ * the trained length:
+ *   SS_ROPE_LINEAR  divided by factor
+ *   SS_ROPE_NTK     base * factor^(rot_dim / (rot_dim - 2)) in base's place
+ *   SS_ROPE_LLAMA3  by the turns n a pair makes over `original` positions:
+ *                   kept for n >= high, divided by factor for n <= low, mixed
+ *                   linearly in n between
+ *   SS_ROPE_YARN    kept for pairs that make more than `high` turns over
+ *                   `original` positions, divided by factor below `low` turns,
+ *                   mixed linearly in the pair's index between; *scale becomes
+ *                   0.1 ln(factor) + 1 (for factor > 1), otherwise 1
+ * scaling may be NULL (none).  base > 1, factor > 0, 0 < low < high. */
+typedef enum {
+    SS_ROPE_NONE = 0,
+    SS_ROPE_LINEAR = 1,
+    SS_ROPE_NTK = 2,
+    SS_ROPE_LLAMA3 = 3,
+    SS_ROPE_YARN = 4
+} ss_rope_kind;
+
+typedef struct {
+    ss_rope_kind kind;
+    double factor;
+    double original; /* length the model was trained on (LLAMA3, YARN) */
+    double low, high; /* turns (LLAMA3: 1 and 4, YARN: 1 and 32 usually) */
+} ss_rope_scaling;
+
+ss_status ss_rope_frequencies(int64_t rot_dim, double base, const ss_rope_scaling *scaling,
+                              double *freqs, double *scale);
 
 /* Returns the first device-side error recorded since the last call
  * (SS_ERR_TIMEOUT, SS_ERR_DATA) or SS_OK, and clears it.  The status word is

@@ -17,14 +17,23 @@ preallocated by the caller):
     ss_get_device_status, ss_status_string, ss_kernel_launches, ss_meta_bytes,
     ss_debug_set_wait_limit, ss_debug_skip_stage (test hooks),
     ss_fp4_shape, ss_fp4_scale_bytes, ss_compress_weight_nvfp4,
-    ss_quant_lift_act_nvfp4, ss_sparse_gemm_nvfp4, ss_dense_gemm_nvfp4
+    ss_quant_lift_act_nvfp4, ss_sparse_gemm_nvfp4, ss_dense_gemm_nvfp4,
+    ss_sparse_gemm_fused, ss_dense_gemm_fused, ss_sparse_gemm_nvfp4_fused,
+    ss_dense_gemm_nvfp4_fused (bias, activation, residual: Epilogue),
+    ss_norm_quant_lift_act, ss_rope, ss_rope_frequencies
 Convenience wrappers that allocate their outputs with torch:
     compress_weight, quant_lift_act, prune_act_2to4, sparse_gemm, dense_gemm,
     linear, and for NVFP4 compress_weight_nvfp4, quant_lift_act_nvfp4,
-    sparse_gemm_nvfp4, dense_gemm_nvfp4, linear_nvfp4
+    sparse_gemm_nvfp4, dense_gemm_nvfp4, linear_nvfp4; the GEMMs and linears
+    take an optional epilogue=Epilogue(...).
+    norm_quant_lift_act, rope, rope_frequencies, interleave_gate_up, and the
+    two halves of a transformer layer around its attention: project_qkv
+    (norm, product, rotary positions), feed_forward (norm, gated product,
+    product into the residual stream).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -46,6 +55,15 @@ SS_IN_F32, SS_IN_BF16 = 0, 1
 SS_INT8, SS_FP8_E4M3, SS_BF16 = 0, 1, 2
 SS_OUT_F32, SS_OUT_BF16 = 0, 1
 
+SS_ACT_NONE, SS_ACT_RELU, SS_ACT_SILU, SS_ACT_GELU, SS_ACT_GELU_ERF = 0, 1, 2, 3, 4
+SS_ROPE_HALF, SS_ROPE_INTERLEAVED = 0, 1
+SS_ROPE_NONE, SS_ROPE_LINEAR, SS_ROPE_NTK, SS_ROPE_LLAMA3, SS_ROPE_YARN = 0, 1, 2, 3, 4
+
+ACTS = {"none": SS_ACT_NONE, "relu": SS_ACT_RELU, "silu": SS_ACT_SILU, "gelu": SS_ACT_GELU,
+        "gelu_erf": SS_ACT_GELU_ERF}
+ROPE_LAYOUTS = {"half": SS_ROPE_HALF, "interleaved": SS_ROPE_INTERLEAVED}
+ROPE_KINDS = {"none": SS_ROPE_NONE, "linear": SS_ROPE_LINEAR, "ntk": SS_ROPE_NTK,
+              "llama3": SS_ROPE_LLAMA3, "yarn": SS_ROPE_YARN}
 QDTYPES = {"int8": SS_INT8, "fp8": SS_FP8_E4M3, "e4m3": SS_FP8_E4M3, "bf16": SS_BF16}
 
 
@@ -57,6 +75,24 @@ class SSError(RuntimeError):
 
 class ss_pattern(ctypes.Structure):
     _fields_ = [("keep", ctypes.c_int32), ("group", ctypes.c_int32)]
+
+
+class ss_epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p),
+                ("bias_dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("act", ctypes.c_int), ("gated", ctypes.c_int32)]
+
+
+class ss_rope_heads(ctypes.Structure):
+    _fields_ = [("in_", ctypes.c_void_p), ("out", ctypes.c_void_p), ("heads", ctypes.c_int64),
+                ("in_token", ctypes.c_int64), ("in_head", ctypes.c_int64),
+                ("out_token", ctypes.c_int64), ("out_head", ctypes.c_int64)]
+
+
+class ss_rope_scaling(ctypes.Structure):
+    _fields_ = [("kind", ctypes.c_int), ("factor", ctypes.c_double),
+                ("original", ctypes.c_double), ("low", ctypes.c_double),
+                ("high", ctypes.c_double)]
 
 
 _lib = None
@@ -91,6 +127,13 @@ def lib() -> ctypes.CDLL:
         "ss_quant_lift_act_nvfp4": [p, i32, i64, i64, pat, i32, p, p, p, p],
         "ss_sparse_gemm_nvfp4": [p, p, p, p, p, p, p, i64, i64, i64, p, i32, p],
         "ss_dense_gemm_nvfp4": [p, p, p, p, p, p, i64, i64, i64, p, i32, p],
+        "ss_sparse_gemm_fused": [i32, p, p, p, p, p, i64, i64, i64, i32, p, p, i32, p],
+        "ss_dense_gemm_fused": [p, p, p, p, i64, i64, i64, i32, p, p, i32, p],
+        "ss_sparse_gemm_nvfp4_fused": [p, p, p, p, p, p, p, i64, i64, i64, p, p, i32, p],
+        "ss_dense_gemm_nvfp4_fused": [p, p, p, p, p, p, i64, i64, i64, p, p, i32, p],
+        "ss_norm_quant_lift_act": [p, i32, p, i32, f, i64, i64, pat, i32, p, p, p],
+        "ss_rope": [p, p, i32, p, ctypes.c_int32, p, f, i64, i64, i64, i32, p],
+        "ss_rope_frequencies": [i64, ctypes.c_double, p, p, p],
     }
     for name, args in sigs.items():
         fn = getattr(L, name)
@@ -104,7 +147,6 @@ def lib() -> ctypes.CDLL:
     L.ss_meta_bytes.restype = i64
     L.ss_fp4_scale_bytes.argtypes = [i64, i64, i32]
     L.ss_fp4_scale_bytes.restype = i64
-    del f
     _lib = L
     return L
 
@@ -302,33 +344,49 @@ def prune_act_2to4(X: torch.Tensor, q, stream=None, out=None):
 
 
 def sparse_gemm(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: int, q,
-                out_dtype=torch.bfloat16, stream=None, out=None):
+                out_dtype=torch.bfloat16, stream=None, out=None, epilogue=None):
     K_lp = Av.shape[1] * 2
+    if epilogue is not None:
+        out = epilogue._out(M, N, out_dtype, Av.device, out)
+        ss_sparse_gemm_fused(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, epilogue, out,
+                             stream)
+        return out
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=Av.device)
     ss_sparse_gemm(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, out, stream)
     return out
 
 
-def dense_gemm(Xq, s_x, Wq, s_w, q, out_dtype=torch.bfloat16, stream=None, out=None):
+def dense_gemm(Xq, s_x, Wq, s_w, q, out_dtype=torch.bfloat16, stream=None, out=None,
+               epilogue=None):
     M, K_p = Xq.shape
     N = Wq.shape[0]
+    if epilogue is not None:
+        out = epilogue._out(M, N, out_dtype, Xq.device, out)
+        ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M, N, K_p, q, epilogue, out, stream)
+        return out
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
     ss_dense_gemm(Xq, s_x, Wq, s_w, M, N, K_p, q, out, stream)
     return out
 
 
-def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream=None):
+def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream=None,
+           epilogue=None, norm=None, out=None):
     """Y = X W^T through the weight-sparse path: quant+lift, then the sparse
-    GEMM (or the dense GEMM for pattern 'dense').  `packed` = compress_weight()."""
+    GEMM (or the dense GEMM for pattern 'dense').  `packed` = compress_weight().
+    norm = (weight, eps): RMS norm of X fused into the quantisation.
+    epilogue: bias, activation and residual fused into the GEMM."""
     Wv, Wm, s_w = packed
     M = X.shape[0]
     N = Wv.shape[0]
-    Xq, s_x = quant_lift_act(X, pattern, q, stream)
+    if norm is None:
+        Xq, s_x = quant_lift_act(X, pattern, q, stream)
+    else:
+        Xq, s_x = norm_quant_lift_act(X, norm[0], norm[1], pattern, q, stream)
     if _pattern(pattern).group == 0:
-        return dense_gemm(Xq, s_x, Wv, s_w, q, out_dtype, stream)
-    return sparse_gemm(0, Wv, Wm, s_w, Xq, s_x, M, N, q, out_dtype, stream)
+        return dense_gemm(Xq, s_x, Wv, s_w, q, out_dtype, stream, out, epilogue)
+    return sparse_gemm(0, Wv, Wm, s_w, Xq, s_x, M, N, q, out_dtype, stream, out, epilogue)
 
 
 # ------------------------------------------------------------------ NVFP4 (pairwise sparse FP4)
@@ -413,10 +471,15 @@ def quant_lift_act_nvfp4(X: torch.Tensor, pattern, block: int, stream=None, out=
 
 
 def sparse_gemm_nvfp4(packed, act, M: int, N: int, out_dtype=torch.bfloat16, stream=None,
-                      out=None):
+                      out=None, epilogue=None):
     Wv, Wm, Ws, g_w = packed
     Xv, Xs, g_x = act
     K_lp = Xv.shape[1] * 2
+    if epilogue is not None:
+        out = epilogue._out(M, N, out_dtype, Xv.device, out)
+        ss_sparse_gemm_nvfp4_fused(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, epilogue, out,
+                                   stream)
+        return out
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=Xv.device)
     ss_sparse_gemm_nvfp4(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, out, stream)
@@ -424,23 +487,339 @@ def sparse_gemm_nvfp4(packed, act, M: int, N: int, out_dtype=torch.bfloat16, str
 
 
 def dense_gemm_nvfp4(act, packed, M: int, N: int, out_dtype=torch.bfloat16, stream=None,
-                     out=None):
+                     out=None, epilogue=None):
     Xv, Xs, g_x = act
     Wv, _, Ws, g_w = packed
     K_p = Xv.shape[1] * 2
+    if epilogue is not None:
+        out = epilogue._out(M, N, out_dtype, Xv.device, out)
+        ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M, N, K_p, epilogue, out, stream)
+        return out
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=Xv.device)
     ss_dense_gemm_nvfp4(Xv, Xs, g_x, Wv, Ws, g_w, M, N, K_p, out, stream)
     return out
 
 
-def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, stream=None):
+def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, stream=None,
+                 epilogue=None, out=None):
     """Y = X W^T in NVFP4: quantisation with one global scale for X + pair
     lift (blocks of 32 for a sparse weight, 16 for a dense one), then the
-    block-scaled GEMM."""
+    block-scaled GEMM, with the fused epilogue if one is given."""
     dense = _pattern(pattern).group == 0
     act = quant_lift_act_nvfp4(X, pattern, 16 if dense else 32, stream)
     M, N = X.shape[0], packed[0].shape[0]
     if dense:
-        return dense_gemm_nvfp4(act, packed, M, N, out_dtype, stream)
-    return sparse_gemm_nvfp4(packed, act, M, N, out_dtype, stream)
+        return dense_gemm_nvfp4(act, packed, M, N, out_dtype, stream, out, epilogue)
+    return sparse_gemm_nvfp4(packed, act, M, N, out_dtype, stream, out, epilogue)
+
+
+# ------------------------------------------------------------------ fused epilogue
+# The calls below check shapes, types and devices (ValueError) before the C
+# call, and run on the device of their tensors, on its current stream, whatever
+# device is current.
+
+def _here(t: torch.Tensor):
+    """Context that makes t's device current (none needed when it already is)."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _raw_stream(stream, t: torch.Tensor) -> int:
+    if stream is None:
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _arg(t, name: str, shape=None, dtypes=None, like=None, contiguous=True) -> int:
+    """Data pointer of a checked CUDA tensor (None stays None)."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError(f"{name} dtype {t.dtype} not supported")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name} is on {t.device}, not {like.device}")
+    return t.data_ptr()
+
+
+_FLOATS = (torch.bfloat16, torch.float32)
+
+
+class Epilogue:
+    """What a GEMM does to its output before the one rounding to Y's type, in
+    fp32: v = dequantised product + bias; Y = act(v) + residual, or, gated,
+    Y = act(gate) * up over weight rows in groups of 16 (eight gates, then
+    the eight rows they multiply: see interleave_gate_up).
+
+    bias [N], residual [M, N]: bf16 or fp32, whatever Y's type; act: "none",
+    "relu", "silu", "gelu" (tanh form) or "gelu_erf".  The residual may be the
+    output tensor itself.  A gated output is [M, N/2] and takes no residual."""
+
+    __slots__ = ("bias", "act", "gated", "residual")
+
+    def __init__(self, bias=None, act="none", gated=False, residual=None):
+        if act not in ACTS:
+            raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
+        self.bias, self.act, self.gated, self.residual = bias, act, bool(gated), residual
+
+    def _out(self, M, N, out_dtype, device, out):
+        if out is not None:
+            return out
+        return torch.empty((M, N // 2 if self.gated else N), dtype=out_dtype, device=device)
+
+    def _args(self, M, N, Y):
+        """(ss_epilogue, Y's pointer), checked against the product's shape."""
+        y = _arg(Y, "Y", (M, N // 2 if self.gated else N), _FLOATS)
+        if y is None:
+            raise ValueError("Y must be a CUDA tensor")
+        e = ss_epilogue(_arg(self.bias, "bias", (N,), _FLOATS, Y),
+                        _arg(self.residual, "residual", (M, N), _FLOATS, Y), SS_IN_BF16,
+                        SS_IN_BF16, ACTS[self.act], int(self.gated))
+        if self.bias is not None:
+            e.bias_dtype = _in_dtype(self.bias)
+        if self.residual is not None:
+            e.residual_dtype = _in_dtype(self.residual)
+        return e, y
+
+
+def _stored(q) -> tuple:
+    """(element types of stored values, scaled?) of an operand of type q."""
+    if q == SS_BF16:
+        return (torch.bfloat16,), False
+    return (torch.uint8, torch.int8, torch.float8_e4m3fn), True
+
+
+def _scale_arg(s, name, n, scaled, like):
+    if not scaled:
+        return None
+    if s is None:
+        raise ValueError(f"{name} is required")
+    return _arg(s, name, (n,), (torch.float32,), like)
+
+
+def ss_sparse_gemm_fused(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: int, K_lp: int, q,
+                         epilogue: Epilogue, Y, stream=None) -> None:
+    q = _qdtype(q)
+    e, y = epilogue._args(M, N, Y)
+    rows_a, rows_b = (M, N) if sparse_operand else (N, M)
+    vals, scaled = _stored(q)
+    a = _arg(Av, "Av", (rows_a, K_lp // 2), vals, Y)
+    m = _arg(Am, "Am", None, (torch.uint8,), Y)
+    if Am is not None and Am.numel() != ss_meta_bytes(rows_a, K_lp):
+        raise ValueError(f"Am must have {ss_meta_bytes(rows_a, K_lp)} bytes, got {Am.numel()}")
+    b = _arg(B, "B", (rows_b, K_lp), vals, Y)
+    sa = _scale_arg(s_a, "s_a", rows_a, scaled, Y)
+    sb = _scale_arg(s_b, "s_b", rows_b, scaled, Y)
+    with _here(Y):
+        _check(lib().ss_sparse_gemm_fused(sparse_operand, a, m, sa, b, sb, M, N, K_lp, q,
+                                          ctypes.byref(e), y, _out_dtype(Y),
+                                          _raw_stream(stream, Y)), "ss_sparse_gemm_fused")
+
+
+def ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M: int, N: int, K_p: int, q, epilogue: Epilogue, Y,
+                        stream=None) -> None:
+    q = _qdtype(q)
+    e, y = epilogue._args(M, N, Y)
+    vals, scaled = _stored(q)
+    x = _arg(Xq, "Xq", (M, K_p), vals, Y)
+    w = _arg(Wq, "Wq", (N, K_p), vals, Y)
+    sx = _scale_arg(s_x, "s_x", M, scaled, Y)
+    sw = _scale_arg(s_w, "s_w", N, scaled, Y)
+    with _here(Y):
+        _check(lib().ss_dense_gemm_fused(x, sx, w, sw, M, N, K_p, q, ctypes.byref(e), y,
+                                         _out_dtype(Y), _raw_stream(stream, Y)),
+               "ss_dense_gemm_fused")
+
+
+def _fp4_arg(t, name, rows, cols, like):
+    return _arg(t, name, (rows, cols), (torch.uint8,), like)
+
+
+def _fp4_scales(s, name, rows, K_lp, block, like):
+    n = ss_fp4_scale_bytes(rows, K_lp, block)
+    if s is not None and s.numel() != n:
+        raise ValueError(f"{name} must have {n} bytes, got {s.numel()}")
+    return _arg(s, name, None, (torch.uint8,), like)
+
+
+def ss_sparse_gemm_nvfp4_fused(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M: int, N: int, K_lp: int,
+                               epilogue: Epilogue, Y, stream=None) -> None:
+    e, y = epilogue._args(M, N, Y)
+    m = _arg(Wm, "Wm", None, (torch.uint8,), Y)
+    if Wm is not None and Wm.numel() != ss_meta_bytes(N, K_lp // 2):
+        raise ValueError(f"Wm must have {ss_meta_bytes(N, K_lp // 2)} bytes, got {Wm.numel()}")
+    args = (_fp4_arg(Wv, "Wv", N, K_lp // 4, Y), m, _fp4_scales(Ws, "Ws", N, K_lp, 32, Y),
+            _arg(g_w, "g_w", None, (torch.float32,), Y), _fp4_arg(Xv, "Xv", M, K_lp // 2, Y),
+            _fp4_scales(Xs, "Xs", M, K_lp, 32, Y), _arg(g_x, "g_x", None, (torch.float32,), Y))
+    with _here(Y):
+        _check(lib().ss_sparse_gemm_nvfp4_fused(*args, M, N, K_lp, ctypes.byref(e), y,
+                                                _out_dtype(Y), _raw_stream(stream, Y)),
+               "ss_sparse_gemm_nvfp4_fused")
+
+
+def ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M: int, N: int, K_p: int,
+                              epilogue: Epilogue, Y, stream=None) -> None:
+    e, y = epilogue._args(M, N, Y)
+    args = (_fp4_arg(Xv, "Xv", M, K_p // 2, Y), _fp4_scales(Xs, "Xs", M, K_p, 16, Y),
+            _arg(g_x, "g_x", None, (torch.float32,), Y), _fp4_arg(Wv, "Wv", N, K_p // 2, Y),
+            _fp4_scales(Ws, "Ws", N, K_p, 16, Y), _arg(g_w, "g_w", None, (torch.float32,), Y))
+    with _here(Y):
+        _check(lib().ss_dense_gemm_nvfp4_fused(*args, M, N, K_p, ctypes.byref(e), y,
+                                               _out_dtype(Y), _raw_stream(stream, Y)),
+               "ss_dense_gemm_nvfp4_fused")
+
+
+def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
+    """The rows of two [F, ...] weights (or biases) as a gated product takes
+    them: groups of eight gates, then their eight partners.  F must be a
+    multiple of 8; compress the result as one weight of 2F rows."""
+    if gate.shape != up.shape or gate.shape[0] % 8 != 0:
+        raise ValueError("gate and up must have the same shape, with a multiple of 8 rows")
+    F = gate.shape[0]
+    both = torch.stack((gate.reshape(F // 8, 8, -1), up.reshape(F // 8, 8, -1)), dim=1)
+    return both.reshape(2 * F, *gate.shape[1:])
+
+
+# ------------------------------------------------------------------ around the products
+
+def ss_norm_quant_lift_act(X, weight, eps: float, pattern, q, Xq_lift, s_x, stream=None) -> None:
+    q = _qdtype(q)
+    x = _arg(X, "X", None, _FLOATS)
+    if X is None or X.dim() != 2:
+        raise ValueError("X must be a [M, K] CUDA tensor")
+    M, K = X.shape
+    _, _, K_lp = ss_slide_shape(pattern, K)
+    vals, scaled = _stored(q)
+    w = _arg(weight, "weight", (K,), _FLOATS, X)
+    if w is None:
+        raise ValueError("weight must be a CUDA tensor")
+    xq = _arg(Xq_lift, "Xq_lift", (M, K_lp), vals, X)
+    sx = _scale_arg(s_x, "s_x", M, scaled, X)
+    with _here(X):
+        _check(lib().ss_norm_quant_lift_act(x, _in_dtype(X), w, _in_dtype(weight), float(eps), M,
+                                            K, _pattern(pattern), q, xq, sx,
+                                            _raw_stream(stream, X)), "ss_norm_quant_lift_act")
+
+
+def norm_quant_lift_act(X: torch.Tensor, weight: torch.Tensor, eps: float, pattern, q,
+                        stream=None, out=None):
+    """RMS norm of X's rows, quantised and lifted as quant_lift_act does;
+    -> (Xq_lift [M, K_lp], s_x [M], or None for the bf16 tier)."""
+    p = _pattern(pattern)
+    if out is None:
+        M, K = X.shape
+        _, _, K_lp = ss_slide_shape(p, K)
+        out = (torch.empty((M, K_lp), dtype=_vals_dtype(q), device=X.device),
+               _scales(M, q, X.device))
+    ss_norm_quant_lift_act(X, weight, eps, p, q, out[0], out[1], stream)
+    return out
+
+
+def ss_rope_frequencies(rot_dim: int, base: float, scaling: ss_rope_scaling | None = None):
+    """-> (rot_dim / 2 frequencies as a list of floats, scale)."""
+    if rot_dim < 2:
+        raise SSError(SS_ERR_INVALID_ARG, "ss_rope_frequencies")
+    f, s = (ctypes.c_double * (rot_dim // 2))(), ctypes.c_double()
+    _check(lib().ss_rope_frequencies(int(rot_dim), float(base),
+                                     None if scaling is None else ctypes.byref(scaling), f,
+                                     ctypes.byref(s)), "ss_rope_frequencies")
+    return list(f), s.value
+
+
+def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "none", factor: float = 1.0,
+                     original: float = 0.0, low: float = 1.0, high: float | None = None,
+                     device="cuda"):
+    """-> (frequencies [rot_dim/2] float64 on `device`, scale) for rope().
+    kind: "none", "linear", "ntk", "llama3" or "yarn" (see ss_rope_scaling);
+    high defaults to 4 turns for llama3 and 32 for yarn."""
+    if kind not in ROPE_KINDS:
+        raise ValueError(f"kind must be one of {sorted(ROPE_KINDS)}, got {kind!r}")
+    if high is None:
+        high = 4.0 if kind == "llama3" else 32.0
+    s = ss_rope_scaling(ROPE_KINDS[kind], factor, original, low, high)
+    f, scale = ss_rope_frequencies(rot_dim, base, s)
+    return torch.tensor(f, dtype=torch.float64, device=device), scale
+
+
+def _heads(x, y, name, T, D, like) -> ss_rope_heads:
+    p = _arg(x, name, None, (like.dtype,), like, contiguous=False)
+    o = _arg(y, f"{name} output", x.shape, (like.dtype,), like, contiguous=False)
+    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
+        raise ValueError(f"{name} must be [{T}, heads, {D}], got {tuple(x.shape)}")
+    for t, what in ((x, name), (y, f"{name} output")):
+        if D > 1 and t.stride(2) != 1:
+            raise ValueError(f"{what}: the elements of a head must be contiguous")
+    if any(n > 1 and s == 0 for n, s in zip(y.shape, y.stride())):
+        raise ValueError(f"{name} output: elements overlap")
+    return ss_rope_heads(p, o, x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+
+
+def ss_rope(q, k, positions, freqs, layout, scale: float, q_out, k_out, stream=None) -> None:
+    if q is None or q.dim() != 3:
+        raise ValueError("q must be a [T, heads, head_dim] CUDA tensor")
+    if (k is None) != (k_out is None):
+        raise ValueError("k and its output go together")
+    layout = ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+    T, _, D = q.shape
+    hq = _heads(q, q_out, "q", T, D, q)
+    hk = None if k is None else _heads(k, k_out, "k", T, D, q)
+    if q.dtype not in _FLOATS:
+        raise ValueError(f"q dtype {q.dtype} not supported (float32 or bfloat16)")
+    pos = _arg(positions, "positions", (T,), (torch.int32, torch.int64), q)
+    f = _arg(freqs, "freqs", None, (torch.float64,), q)
+    if pos is None or f is None:
+        raise ValueError("positions and freqs must be CUDA tensors")
+    with _here(q):
+        _check(lib().ss_rope(ctypes.byref(hq), None if hk is None else ctypes.byref(hk),
+                             _in_dtype(q), pos, int(positions.dtype == torch.int64), f,
+                             float(scale), T, D, 2 * freqs.numel(), layout,
+                             _raw_stream(stream, q)), "ss_rope")
+
+
+def rope(q: torch.Tensor, k, positions: torch.Tensor, freqs: torch.Tensor, layout="half",
+         scale: float = 1.0, stream=None, out=None):
+    """Rotary positions of q [T, Hq, D] and k [T, Hk, D] (or None), which may be
+    strided views into a projection's output; -> (q', k').  The first
+    2 * len(freqs) elements of each head turn; freqs and scale come from
+    rope_frequencies.  out = (q, k): in place."""
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    ss_rope(q, k, positions, freqs, layout, scale, out[0], out[1], stream)
+    return out
+
+
+def project_qkv(X: torch.Tensor, packed, pattern, q, heads: int, kv_heads: int, positions, freqs,
+                layout="half", scale: float = 1.0, norm=None, bias=None, stream=None):
+    """The attention's inputs of a transformer layer: RMS norm of X (norm =
+    (weight, eps) or None) fused into its quantisation, the fused query / key /
+    value product with its bias, and rotary positions on the query and key
+    heads in place.  The weight's rows are (heads + 2 kv_heads) heads of equal
+    size.  -> q [M, heads, D], k, v [M, kv_heads, D], views of one tensor."""
+    N = packed[0].shape[0]
+    if N % (heads + 2 * kv_heads) != 0:
+        raise ValueError(f"{N} rows are not {heads} + 2 * {kv_heads} heads")
+    Y = linear(X, packed, pattern, q, stream=stream, norm=norm,
+               epilogue=None if bias is None else Epilogue(bias=bias))
+    Y = Y.view(X.shape[0], heads + 2 * kv_heads, -1)
+    yq, yk, yv = Y.split((heads, kv_heads, kv_heads), dim=1)
+    rope(yq, yk, positions, freqs, layout, scale, stream, out=(yq, yk))
+    return yq, yk, yv
+
+
+def feed_forward(X: torch.Tensor, packed_gate_up, packed_down, pattern, q, act="silu", norm=None,
+                 stream=None):
+    """The feed-forward half of a transformer layer, X + down(act(gate) * up)
+    with gate, up of the RMS norm of X (norm = (weight, eps) or None):
+    `packed_gate_up` = compress_weight(interleave_gate_up(W_gate, W_up)).
+    -> [M, K] of X's type."""
+    h = linear(X, packed_gate_up, pattern, q, stream=stream, norm=norm,
+               epilogue=Epilogue(act=act, gated=True))
+    return linear(h, packed_down, pattern, q, X.dtype, stream, Epilogue(residual=X))

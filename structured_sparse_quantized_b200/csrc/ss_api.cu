@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <cmath>
 #include <cstdint>
 #include <cstdlib>
 #include <cstring>
@@ -19,7 +20,9 @@
 #include "ss_gemm.cuh"
 #include "ss_gemm_splitk.cuh"
 #include "ss_gemm_wide.cuh"
+#include "ss_norm.cuh"
 #include "ss_quant.cuh"
+#include "ss_rope.cuh"
 
 namespace {
 
@@ -159,13 +162,13 @@ bool make_y_map(CUtensorMap* map, void* Y, int64_t M, int64_t N, bool out_bf16, 
                   : make_map_2d(map, Y, M, N, ss::kTileA, 32, CU_TENSOR_MAP_SWIZZLE_NONE, dt, esz);
 }
 
-template <bool kSparse, int kQ, bool kOutBf16, int kPair>
+template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi>
 ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& e,
                       const CUtensorMap& y, const ss::GemmArgs& args, cudaStream_t stream,
                       const CUtensorMap* sfa = nullptr, const CUtensorMap* sfb = nullptr) {
     using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair>,
                                  ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1>>;
-    auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair>;
+    auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
     std::call_once(once[dev], [&] {
@@ -183,28 +186,64 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
 }
 
 // q: ss::kQE4M3, kQInt8 or kQBf16; bf16: Y element type.
-template <bool kSparse, int kPair>
+template <bool kSparse, int kPair, bool kEpi>
 ss_status dispatch_gemm(int dev, int q, bool bf16, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& e, const CUtensorMap& y, const ss::GemmArgs& args,
                         cudaStream_t st) {
     using namespace ss;
     if (q == kQInt8)
-        return bf16 ? launch_gemm<kSparse, kQInt8, true, kPair>(dev, a, b, e, y, args, st)
-                    : launch_gemm<kSparse, kQInt8, false, kPair>(dev, a, b, e, y, args, st);
+        return bf16 ? launch_gemm<kSparse, kQInt8, true, kPair, kEpi>(dev, a, b, e, y, args, st)
+                    : launch_gemm<kSparse, kQInt8, false, kPair, kEpi>(dev, a, b, e, y, args, st);
     if (q == kQBf16)
-        return bf16 ? launch_gemm<kSparse, kQBf16, true, kPair>(dev, a, b, e, y, args, st)
-                    : launch_gemm<kSparse, kQBf16, false, kPair>(dev, a, b, e, y, args, st);
-    return bf16 ? launch_gemm<kSparse, kQE4M3, true, kPair>(dev, a, b, e, y, args, st)
-                : launch_gemm<kSparse, kQE4M3, false, kPair>(dev, a, b, e, y, args, st);
+        return bf16 ? launch_gemm<kSparse, kQBf16, true, kPair, kEpi>(dev, a, b, e, y, args, st)
+                    : launch_gemm<kSparse, kQBf16, false, kPair, kEpi>(dev, a, b, e, y, args, st);
+    return bf16 ? launch_gemm<kSparse, kQE4M3, true, kPair, kEpi>(dev, a, b, e, y, args, st)
+                : launch_gemm<kSparse, kQE4M3, false, kPair, kEpi>(dev, a, b, e, y, args, st);
+}
+
+template <bool kSparse>
+ss_status dispatch_gemm_any(int dev, int q, bool bf16, int pair, bool fused, const CUtensorMap& a,
+                            const CUtensorMap& b, const CUtensorMap& e, const CUtensorMap& y,
+                            const ss::GemmArgs& args, cudaStream_t st) {
+    if (pair == 1)
+        return fused ? dispatch_gemm<kSparse, 1, true>(dev, q, bf16, a, b, e, y, args, st)
+                     : dispatch_gemm<kSparse, 1, false>(dev, q, bf16, a, b, e, y, args, st);
+    return fused ? dispatch_gemm<kSparse, 2, true>(dev, q, bf16, a, b, e, y, args, st)
+                 : dispatch_gemm<kSparse, 2, false>(dev, q, bf16, a, b, e, y, args, st);
+}
+
+// The fused epilogue `epi` of a product with N output channels, checked; with
+// epi null or nothing in it, *fused is false and the plain kernels run.
+ss_status check_epilogue(const ss_epilogue* epi, int64_t N, ss::EpiArgs* out, bool* fused) {
+    *out = ss::EpiArgs{};
+    *fused = false;
+    if (!epi) return SS_OK;
+    if (epi->act < SS_ACT_NONE || epi->act > SS_ACT_GELU_ERF ||
+        (epi->gated != 0 && epi->gated != 1))
+        return SS_ERR_INVALID_ARG;
+    for (const ss_in_dtype d : {epi->bias ? epi->bias_dtype : SS_IN_BF16,
+                                epi->residual ? epi->residual_dtype : SS_IN_BF16})
+        if (d != SS_IN_F32 && d != SS_IN_BF16) return SS_ERR_INVALID_ARG;
+    if (epi->gated && N % 16 != 0) return SS_ERR_INVALID_ARG;
+    if (epi->gated && epi->residual) return SS_ERR_UNSUPPORTED;
+    if (!aligned16(epi->bias) || !aligned16(epi->residual)) return SS_ERR_ALIGNMENT;
+    out->bias = epi->bias;
+    out->residual = epi->residual;
+    out->bias_f32 = epi->bias && epi->bias_dtype == SS_IN_F32;
+    out->res_f32 = epi->residual && epi->residual_dtype == SS_IN_F32;
+    out->act = epi->act;
+    out->gated = epi->gated;
+    *fused = epi->bias || epi->residual || epi->act != SS_ACT_NONE || epi->gated;
+    return SS_OK;
 }
 
 // Split-K GEMM (decode sizes, A = weight): S K parts on the S CTAs of a
 // cluster.  Returns the number of clusters of S CTAs that can be resident at
 // once (0 if the kernel cannot run), cached per device.
-template <bool kSparse, int kQ, bool kOutBf16>
+template <bool kSparse, int kQ, bool kOutBf16, bool kEpi>
 int splitk_max_clusters(int dev, int S) {
     using C = ss::SplitKCfg<kSparse, kQ == ss::kQBf16 ? 2 : 1>;
-    auto kern = ss::gemm_splitk_kernel<kSparse, kQ, kOutBf16>;
+    auto kern = ss::gemm_splitk_kernel<kSparse, kQ, kOutBf16, kEpi>;
     static std::once_flag once[kMaxDevices];
     static int cached[kMaxDevices][4];  // S = 2, 4, 8
     std::call_once(once[dev], [&] {
@@ -237,11 +276,11 @@ int splitk_max_clusters(int dev, int S) {
     return S == 2 ? cached[dev][1] : (S == 4 ? cached[dev][2] : (S == 8 ? cached[dev][3] : 0));
 }
 
-template <bool kSparse, int kQ, bool kOutBf16>
+template <bool kSparse, int kQ, bool kOutBf16, bool kEpi>
 ss_status launch_splitk(int S, int64_t tiles, const CUtensorMap& a, const CUtensorMap& b,
                         const CUtensorMap& e, const ss::GemmArgs& args, cudaStream_t stream) {
     using C = ss::SplitKCfg<kSparse, kQ == ss::kQBf16 ? 2 : 1>;
-    return launch_ex(ss::gemm_splitk_kernel<kSparse, kQ, kOutBf16>,
+    return launch_ex(ss::gemm_splitk_kernel<kSparse, kQ, kOutBf16, kEpi>,
                      dim3(static_cast<unsigned>(tiles * S)), dim3(ss::kSplitKThreads), C::kSmemBytes,
                      stream, S, a, b, e, args);
 }
@@ -250,7 +289,7 @@ ss_status launch_splitk(int S, int64_t tiles, const CUtensorMap& a, const CUtens
 // tile of at most ss::kSkBn): the largest S in {8, 4, 2} whose tiles x S CTAs
 // are all resident at once, with at least one K stage per part, and which
 // keeps more SMs busy than the one-pass kernel's CTA pairs.  0: no split.
-template <bool kSparse, int kQ, bool kOutBf16>
+template <bool kSparse, int kQ, bool kOutBf16, bool kEpi>
 int choose_split(int dev, int64_t rowsA, int64_t rowsB, int k_stages) {
     if (rowsB > ss::kSkBn) return 0;
     const int64_t tiles = (rowsA + ss::kTileA - 1) / ss::kTileA;
@@ -258,20 +297,20 @@ int choose_split(int dev, int64_t rowsA, int64_t rowsB, int k_stages) {
                                                  : 1;
     for (int S = 8; S >= 2; S /= 2) {
         if (S > k_stages || tiles * S > g_num_sms[dev] || tiles * S <= pair_ctas) continue;
-        if (tiles <= splitk_max_clusters<kSparse, kQ, kOutBf16>(dev, S)) return S;
+        if (tiles <= splitk_max_clusters<kSparse, kQ, kOutBf16, kEpi>(dev, S)) return S;
     }
     return 0;
 }
 
 // Split-K dispatch on the operand type and Y type; returns SS_ERR_UNSUPPORTED
 // (nothing launched) when no split applies.
-template <bool kSparse>
+template <bool kSparse, bool kEpi>
 ss_status try_splitk(int dev, int q, bool bf16, int64_t rowsA, int64_t rowsB,
                      const void* Av, int64_t a_cols, const void* B, int64_t b_cols,
                      const CUtensorMap& e, const ss::GemmArgs& args, cudaStream_t stream) {
     using namespace ss;
     int S = 0;
-#define SS_SK_PICK(Q, BF) S = choose_split<kSparse, Q, BF>(dev, rowsA, rowsB, args.k_stages)
+#define SS_SK_PICK(Q, BF) S = choose_split<kSparse, Q, BF, kEpi>(dev, rowsA, rowsB, args.k_stages)
     if (q == kQInt8) { if (bf16) SS_SK_PICK(kQInt8, true); else SS_SK_PICK(kQInt8, false); }
     else if (q == kQBf16) { if (bf16) SS_SK_PICK(kQBf16, true); else SS_SK_PICK(kQBf16, false); }
     else { if (bf16) SS_SK_PICK(kQE4M3, true); else SS_SK_PICK(kQE4M3, false); }
@@ -284,7 +323,7 @@ ss_status try_splitk(int dev, int q, bool bf16, int64_t rowsA, int64_t rowsB,
         !make_map_2d(&tb, B, rowsB, b_cols, a2.bn, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return SS_ERR_CUDA;
     const int64_t tiles = (rowsA + ss::kTileA - 1) / ss::kTileA;
-#define SS_SK_GO(Q, BF) return launch_splitk<kSparse, Q, BF>(S, tiles, ta, tb, e, a2, stream)
+#define SS_SK_GO(Q, BF) return launch_splitk<kSparse, Q, BF, kEpi>(S, tiles, ta, tb, e, a2, stream)
     if (q == kQInt8) { if (bf16) SS_SK_GO(kQInt8, true); SS_SK_GO(kQInt8, false); }
     if (q == kQBf16) { if (bf16) SS_SK_GO(kQBf16, true); SS_SK_GO(kQBf16, false); }
     if (bf16) SS_SK_GO(kQE4M3, true);
@@ -484,9 +523,15 @@ int64_t ss_meta_bytes(int64_t rows, int64_t K_lp) {
     return (rows + 127) / 128 * 128 * (K_lp / 8);
 }
 
-ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, const float* s_a,
-                         const void* B, const float* s_b, int64_t M, int64_t N, int64_t K_lp,
-                         ss_qdtype q, void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// ss_sparse_gemm and ss_sparse_gemm_fused (epi null: no fused epilogue).
+ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const float* s_a,
+                      const void* B, const float* s_b, int64_t M, int64_t N, int64_t K_lp,
+                      ss_qdtype q, const ss_epilogue* epi, void* Y, ss_out_dtype out_dtype,
+                      ss_stream_t stream) {
     if (sparse_operand != 0 && sparse_operand != 1) return SS_ERR_INVALID_ARG;
     const int kq = kernel_q(q);
     if (kq < 0) return SS_ERR_INVALID_ARG;
@@ -497,9 +542,12 @@ ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, con
         return SS_ERR_INVALID_ARG;
     if (out_dtype != SS_OUT_F32 && out_dtype != SS_OUT_BF16) return SS_ERR_INVALID_ARG;
     if (!aligned16(Av) || !aligned16(Am) || !aligned16(B) || !aligned16(Y)) return SS_ERR_ALIGNMENT;
-    int dev;
-    ss_status st = check_device(&dev);
+    ss::GemmArgs args;
+    bool fused;
+    ss_status st = check_epilogue(epi, N, &args.epi, &fused);
     if (st != SS_OK) return st;
+    int dev;
+    if ((st = check_device(&dev)) != SS_OK) return st;
     const int64_t rowsA = sparse_operand == 0 ? N : M;
     const int64_t rowsB = sparse_operand == 0 ? M : N;
     const int pair = rowsA > ss::kTileA ? 2 : 1;
@@ -515,7 +563,6 @@ ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, con
         !make_map_2d(&te, Am, (rowsA + 127) / 128 * (K_lp / 128) * 16, 128, 16, 128,
                      CU_TENSOR_MAP_SWIZZLE_NONE))
         return SS_ERR_CUDA;
-    ss::GemmArgs args;
     args.rowsA = static_cast<int>(rowsA);
     args.rowsB = static_cast<int>(rowsB);
     // 8-bit: a last half stage (K_lp an odd multiple of 128) reads zeros past
@@ -524,7 +571,7 @@ ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, con
     args.k_stages = static_cast<int>((K_lp + stage_k - 1) / stage_k);
     args.bn = bn;
     args.a_is_w = sparse_operand == 0 ? 1 : 0;
-    args.ldy = static_cast<int>(N);
+    args.ldy = static_cast<int>(args.epi.gated ? N / 2 : N);
     args.e_chunks = static_cast<int>(K_lp / 128);
     args.sf_k = 0;
     // values + selectors of A; B tiles of bn rows (the wide kernel sets its own)
@@ -534,21 +581,23 @@ ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, con
     args.s_b = s_b;
     args.y = Y;
     CUtensorMap ty;
-    args.tma_store = make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, args.a_is_w) ? 1 : 0;
+    args.tma_store =
+        !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, args.a_is_w) ? 1 : 0;
     if (!args.tma_store) ty = ta;  // unused
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool i8 = q == SS_INT8, bf = out_dtype == SS_OUT_BF16;
     const int forced = forced_sparse_kernel();
     if (args.a_is_w && forced != 1 && forced != 2) {  // decode sizes: split K over a cluster
-        const ss_status sk = try_splitk<true>(dev, kq, bf, rowsA, rowsB, Av, K_lp / 2 * eb, B,
-                                              K_lp * eb, te, args, st_);
+        auto split = fused ? try_splitk<true, true> : try_splitk<true, false>;
+        const ss_status sk =
+            split(dev, kq, bf, rowsA, rowsB, Av, K_lp / 2 * eb, B, K_lp * eb, te, args, st_);
         if (sk != SS_ERR_UNSUPPORTED) return sk;
     }
 #if SS_SPARSE_WIDE
     // (8-bit operands only: the bf16 tier runs the one-B-tile kernel)
     // Large problems with bf16 Y may take two B tiles per output tile: fewer
     // bytes per MMA, but single-buffered accumulators.
-    if (scaled && pair == 2 && args.tma_store && forced != 1 &&
+    if (scaled && !fused && pair == 2 && args.tma_store && forced != 1 &&
         (forced == 2 || (rowsB > 2 * ss::WideCfg::kBnMax &&
                          prefer_wide(rowsA, rowsB, bn, g_num_sms[dev] / 2)))) {
         using CW = ss::WideCfg;
@@ -570,13 +619,13 @@ ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, con
                   : launch_gemm_wide<false, false>(dev, wa, wb, te, ty, wargs, st_);
     }
 #endif
-    if (pair == 1) return dispatch_gemm<true, 1>(dev, kq, bf, ta, tb, te, ty, args, st_);
-    return dispatch_gemm<true, 2>(dev, kq, bf, ta, tb, te, ty, args, st_);
+    return dispatch_gemm_any<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, args, st_);
 }
 
-ss_status ss_dense_gemm(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
-                        int64_t M, int64_t N, int64_t K_p, ss_qdtype q, void* Y,
-                        ss_out_dtype out_dtype, ss_stream_t stream) {
+// ss_dense_gemm and ss_dense_gemm_fused.
+ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
+                     int64_t M, int64_t N, int64_t K_p, ss_qdtype q, const ss_epilogue* epi,
+                     void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
     const int kq = kernel_q(q);
     if (kq < 0) return SS_ERR_INVALID_ARG;
     const bool scaled = kq != ss::kQBf16;  // bf16 tier: s_x, s_w unused
@@ -586,9 +635,12 @@ ss_status ss_dense_gemm(const void* Xq, const float* s_x, const void* Wq, const 
         return SS_ERR_INVALID_ARG;
     if (out_dtype != SS_OUT_F32 && out_dtype != SS_OUT_BF16) return SS_ERR_INVALID_ARG;
     if (!aligned16(Xq) || !aligned16(Wq) || !aligned16(Y)) return SS_ERR_ALIGNMENT;
-    int dev;
-    ss_status st = check_device(&dev);
+    ss::GemmArgs args;
+    bool fused;
+    ss_status st = check_epilogue(epi, N, &args.epi, &fused);
     if (st != SS_OK) return st;
+    int dev;
+    if ((st = check_device(&dev)) != SS_OK) return st;
     const int pair = N > ss::kTileA ? 2 : 1;
     const int bn = choose_bn(M, ss::GemmCfg<false, 1>::kBnMax);
     if (tiles_overflow(N, M, bn)) return SS_ERR_UNSUPPORTED;
@@ -597,13 +649,12 @@ ss_status ss_dense_gemm(const void* Xq, const float* s_x, const void* Wq, const 
     if (!make_map_2d(&ta, Wq, N, K_p * eb, ss::kTileA, 128, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_map_2d(&tb, Xq, M, K_p * eb, bn / pair, 128, CU_TENSOR_MAP_SWIZZLE_128B))
         return SS_ERR_CUDA;
-    ss::GemmArgs args;
     args.rowsA = static_cast<int>(N);
     args.rowsB = static_cast<int>(M);
     args.k_stages = static_cast<int>(K_p * eb / 128);  // 128 bytes of K per stage
     args.bn = bn;
     args.a_is_w = 1;
-    args.ldy = static_cast<int>(N);
+    args.ldy = static_cast<int>(args.epi.gated ? N / 2 : N);
     args.e_chunks = 0;
     args.sf_k = 0;
     args.a_groups = a_groups_for(N * K_p * eb, (N + 255) / 256, g_num_sms[dev] / 2,
@@ -612,17 +663,49 @@ ss_status ss_dense_gemm(const void* Xq, const float* s_x, const void* Wq, const 
     args.s_b = s_x;
     args.y = Y;
     CUtensorMap ty;
-    args.tma_store = make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
+    args.tma_store = !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
     if (!args.tma_store) ty = ta;  // unused
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = out_dtype == SS_OUT_BF16;
     if (forced_sparse_kernel() != 1) {  // decode sizes: split K over a cluster
+        auto split = fused ? try_splitk<false, true> : try_splitk<false, false>;
         const ss_status sk =
-            try_splitk<false>(dev, kq, bf, N, M, Wq, K_p * eb, Xq, K_p * eb, ta, args, st_);
+            split(dev, kq, bf, N, M, Wq, K_p * eb, Xq, K_p * eb, ta, args, st_);
         if (sk != SS_ERR_UNSUPPORTED) return sk;
     }
-    return pair == 2 ? dispatch_gemm<false, 2>(dev, kq, bf, ta, tb, ta, ty, args, st_)
-                     : dispatch_gemm<false, 1>(dev, kq, bf, ta, tb, ta, ty, args, st_);
+    return dispatch_gemm_any<false>(dev, kq, bf, pair, fused, ta, tb, ta, ty, args, st_);
+}
+
+}  // namespace
+
+extern "C" {
+
+ss_status ss_sparse_gemm(int sparse_operand, const void* Av, const void* Am, const float* s_a,
+                         const void* B, const float* s_b, int64_t M, int64_t N, int64_t K_lp,
+                         ss_qdtype q, void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
+    return sparse_gemm(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, nullptr, Y, out_dtype,
+                       stream);
+}
+
+ss_status ss_sparse_gemm_fused(int sparse_operand, const void* Av, const void* Am,
+                               const float* s_a, const void* B, const float* s_b, int64_t M,
+                               int64_t N, int64_t K_lp, ss_qdtype q, const ss_epilogue* epi,
+                               void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
+    return sparse_gemm(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, epi, Y, out_dtype,
+                       stream);
+}
+
+ss_status ss_dense_gemm(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
+                        int64_t M, int64_t N, int64_t K_p, ss_qdtype q, void* Y,
+                        ss_out_dtype out_dtype, ss_stream_t stream) {
+    return dense_gemm(Xq, s_x, Wq, s_w, M, N, K_p, q, nullptr, Y, out_dtype, stream);
+}
+
+ss_status ss_dense_gemm_fused(const void* Xq, const float* s_x, const void* Wq, const float* s_w,
+                              int64_t M, int64_t N, int64_t K_p, ss_qdtype q,
+                              const ss_epilogue* epi, void* Y, ss_out_dtype out_dtype,
+                              ss_stream_t stream) {
+    return dense_gemm(Xq, s_x, Wq, s_w, M, N, K_p, q, epi, Y, out_dtype, stream);
 }
 
 // ---------------------------------------------------------------- NVFP4
@@ -661,7 +744,8 @@ namespace {
 template <bool kSparse>
 ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float* g_w,
                      const void* Bv, const void* Bs, const float* g_x, int64_t M, int64_t N,
-                     int64_t K_lp, void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
+                     int64_t K_lp, const ss_epilogue* epi, void* Y, ss_out_dtype out_dtype,
+                     ss_stream_t stream) {
     if (!Av || (kSparse && !Am) || !As || !g_w || !Bv || !Bs || !g_x || !Y)
         return SS_ERR_INVALID_ARG;
     if (M <= 0 || N <= 0 || M > INT32_MAX || N > INT32_MAX || K_lp <= 0 || K_lp % 256 != 0 ||
@@ -671,9 +755,12 @@ ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float
     if (!aligned16(Av) || (kSparse && !aligned16(Am)) || !aligned16(As) || !aligned16(Bv) ||
         !aligned16(Bs) || !aligned16(Y))
         return SS_ERR_ALIGNMENT;
-    int dev;
-    ss_status st = check_device(&dev);
+    ss::GemmArgs args;
+    bool fused;
+    ss_status st = check_epilogue(epi, N, &args.epi, &fused);
     if (st != SS_OK) return st;
+    int dev;
+    if ((st = check_device(&dev)) != SS_OK) return st;
     using C = ss::Fp4Cfg<kSparse>;
     const int block = kSparse ? 32 : 16;
     // CTA pairs (MMA M = 256, N up to 256 tokens) above one 128-row A tile;
@@ -701,13 +788,12 @@ ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float
     } else {
         te = ta;  // unused
     }
-    ss::GemmArgs args;
     args.rowsA = static_cast<int>(N);
     args.rowsB = static_cast<int>(M);
     args.k_stages = static_cast<int>((K_lp + C::kStageK - 1) / C::kStageK);
     args.bn = bn;
     args.a_is_w = 1;
-    args.ldy = static_cast<int>(N);
+    args.ldy = static_cast<int>(args.epi.gated ? N / 2 : N);
     args.e_chunks = static_cast<int>(K_lp / 256);
     args.sf_k = static_cast<int>(nblk / 4);
     // codes, block scales and (sparse) selectors of the weight
@@ -718,18 +804,22 @@ ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float
     args.s_b = g_x;
     args.y = Y;
     CUtensorMap ty;
-    args.tma_store = make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
+    args.tma_store = !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
     if (!args.tma_store) ty = ta;  // unused
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = out_dtype == SS_OUT_BF16;
-    if (pair == 2)
-        return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, 2>(dev, ta, tb, te, ty, args, st_, &tsa,
-                                                               &tsb)
-                  : launch_gemm<kSparse, ss::kQNvfp4, false, 2>(dev, ta, tb, te, ty, args, st_,
-                                                                &tsa, &tsb);
-    return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, 1>(dev, ta, tb, te, ty, args, st_, &tsa, &tsb)
-              : launch_gemm<kSparse, ss::kQNvfp4, false, 1>(dev, ta, tb, te, ty, args, st_, &tsa,
-                                                            &tsb);
+#define SS_FP4_GO(P, E)                                                                       \
+    return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, P, E>(dev, ta, tb, te, ty, args, st_, \
+                                                              &tsa, &tsb)                     \
+              : launch_gemm<kSparse, ss::kQNvfp4, false, P, E>(dev, ta, tb, te, ty, args,     \
+                                                               st_, &tsa, &tsb)
+    if (pair == 2) {
+        if (fused) SS_FP4_GO(2, true);
+        SS_FP4_GO(2, false);
+    }
+    if (fused) SS_FP4_GO(1, true);
+    SS_FP4_GO(1, false);
+#undef SS_FP4_GO
 }
 
 }  // namespace
@@ -740,13 +830,31 @@ ss_status ss_sparse_gemm_nvfp4(const void* Wv, const void* Wm, const void* Ws, c
                                const void* Xv, const void* Xs, const float* g_x, int64_t M,
                                int64_t N, int64_t K_lp, void* Y, ss_out_dtype out_dtype,
                                ss_stream_t stream) {
-    return gemm_nvfp4<true>(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, Y, out_dtype, stream);
+    return gemm_nvfp4<true>(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, nullptr, Y, out_dtype,
+                            stream);
+}
+
+ss_status ss_sparse_gemm_nvfp4_fused(const void* Wv, const void* Wm, const void* Ws,
+                                     const float* g_w, const void* Xv, const void* Xs,
+                                     const float* g_x, int64_t M, int64_t N, int64_t K_lp,
+                                     const ss_epilogue* epi, void* Y, ss_out_dtype out_dtype,
+                                     ss_stream_t stream) {
+    return gemm_nvfp4<true>(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, epi, Y, out_dtype, stream);
 }
 
 ss_status ss_dense_gemm_nvfp4(const void* Xv, const void* Xs, const float* g_x, const void* Wv,
                               const void* Ws, const float* g_w, int64_t M, int64_t N,
                               int64_t K_p, void* Y, ss_out_dtype out_dtype, ss_stream_t stream) {
-    return gemm_nvfp4<false>(Wv, nullptr, Ws, g_w, Xv, Xs, g_x, M, N, K_p, Y, out_dtype, stream);
+    return gemm_nvfp4<false>(Wv, nullptr, Ws, g_w, Xv, Xs, g_x, M, N, K_p, nullptr, Y, out_dtype,
+                             stream);
+}
+
+ss_status ss_dense_gemm_nvfp4_fused(const void* Xv, const void* Xs, const float* g_x,
+                                    const void* Wv, const void* Ws, const float* g_w, int64_t M,
+                                    int64_t N, int64_t K_p, const ss_epilogue* epi, void* Y,
+                                    ss_out_dtype out_dtype, ss_stream_t stream) {
+    return gemm_nvfp4<false>(Wv, nullptr, Ws, g_w, Xv, Xs, g_x, M, N, K_p, epi, Y, out_dtype,
+                             stream);
 }
 
 ss_status ss_get_device_status(ss_stream_t stream) {
@@ -791,3 +899,7 @@ ss_status ss_debug_skip_stage(int32_t kb) {
 // The entry points that prepare the GEMM operands (weight compression,
 // activation quantisation, lifting and pruning, and their NVFP4 forms).
 #include "ss_api_operands.cuh"
+
+// The entry points for what surrounds the products in a layer (rotary
+// positions, the norm fused into the quantisation).
+#include "ss_api_layer.cuh"

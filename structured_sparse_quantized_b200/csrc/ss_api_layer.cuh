@@ -1,0 +1,178 @@
+// ss_api_layer.cuh -- the C entry points of libss (declared in include/ss.h)
+// for what a transformer layer does around its products: rotary positions
+// (ss_rope, ss_rope_frequencies) and the RMS norm fused into the activation's
+// quantisation (ss_norm_quant_lift_act).  Included once, at the end of
+// ss_api.cu, whose host helpers (device checks, launches) it uses.
+#pragma once
+
+namespace {
+
+template <typename T, int V, bool kHalf>
+ss_status launch_rope(ss::RopeArgs a, cudaStream_t s) {
+    const int64_t heads = static_cast<int64_t>(a.t[0].heads) + a.t[1].heads;
+    const int pairs = kHalf ? V : (V > 1 ? V / 2 : 1);
+    a.rot_units = a.rot / 2 / pairs;
+    bool in_place = true;
+    for (const ss::RopeTensor& t : a.t)
+        in_place = in_place && (t.heads == 0 || (t.in == t.out && t.in_token == t.out_token &&
+                                                 t.in_head == t.out_head));
+    a.units = a.rot_units + (in_place ? 0 : (a.D - a.rot) / V);
+    // about four units per thread
+    const int64_t per_token = heads * a.units;
+    a.tokens = static_cast<int>(std::min<int64_t>(
+        std::max<int64_t>(4 * ss::kRopeThreads / per_token, 1), ss::kRopeMaxTokens));
+    const size_t smem = static_cast<size_t>(a.tokens) * (a.rot / 2) * sizeof(float2);
+    const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
+    return launch_ex(ss::rope_kernel<T, V, kHalf>, dim3(grid), dim3(ss::kRopeThreads), smem, s, 1,
+                     a);
+}
+
+template <typename T>
+ss_status dispatch_rope(const ss::RopeArgs& a, bool half, cudaStream_t s) {
+    // 16-byte accesses need every row start and every unit on a 16-byte boundary
+    constexpr int V = 16 / static_cast<int>(sizeof(T));
+    bool vec = (a.D - a.rot) % V == 0 && (half ? a.rot / 2 : a.rot) % V == 0;
+    for (const ss::RopeTensor& t : a.t)
+        if (t.heads)
+            vec = vec && aligned16(t.in) && aligned16(t.out) && t.in_token % V == 0 &&
+                  t.in_head % V == 0 && t.out_token % V == 0 && t.out_head % V == 0;
+    if (half)
+        return vec ? launch_rope<T, V, true>(a, s) : launch_rope<T, 1, true>(a, s);
+    return vec ? launch_rope<T, V, false>(a, s) : launch_rope<T, 1, false>(a, s);
+}
+
+template <typename T, int kQ>
+ss_status launch_norm(const void* X, const void* w, int wf32, float eps, int64_t M, int64_t K,
+                      int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
+                      cudaStream_t s) {
+    return launch_ex(ss::norm_quant_lift_kernel<T, kQ>, dim3(static_cast<unsigned>(M)),
+                     dim3(ss::kWarpRowThreads), 0, s, 1, static_cast<const T*>(X), w, wf32, eps, M,
+                     static_cast<int>(K), Nh, static_cast<int>(K_lift), static_cast<int>(K_lp),
+                     static_cast<uint8_t*>(Xq), s_x);
+}
+
+}  // namespace
+
+extern "C" {
+
+ss_status ss_rope_frequencies(int64_t rot_dim, double base, const ss_rope_scaling* scaling,
+                              double* freqs, double* scale) {
+    if (rot_dim < 2 || rot_dim % 2 != 0 || rot_dim > ss::kRopeMaxDim || !freqs || !scale)
+        return SS_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !std::isfinite(base)) return SS_ERR_INVALID_ARG;
+    const ss_rope_scaling none = {SS_ROPE_NONE, 1.0, 1.0, 1.0, 1.0};
+    const ss_rope_scaling& s = scaling ? *scaling : none;
+    if (s.kind < SS_ROPE_NONE || s.kind > SS_ROPE_YARN) return SS_ERR_INVALID_ARG;
+    if (s.kind != SS_ROPE_NONE && (!(s.factor > 0.0) || !std::isfinite(s.factor)))
+        return SS_ERR_INVALID_ARG;
+    const bool banded = s.kind == SS_ROPE_LLAMA3 || s.kind == SS_ROPE_YARN;
+    if (banded && (!(s.original > 0.0) || !std::isfinite(s.original) || !(s.low > 0.0) ||
+                   !(s.high > s.low) || !std::isfinite(s.high)))
+        return SS_ERR_INVALID_ARG;
+    constexpr double kTwoPi = 6.283185307179586477;
+    const double d = static_cast<double>(rot_dim);
+    double b = base;
+    if (s.kind == SS_ROPE_NTK && rot_dim > 2) b = base * std::pow(s.factor, d / (d - 2.0));
+    double first = 0.0, last = 1.0;  // YaRN: pairs between which the two scalings mix
+    if (s.kind == SS_ROPE_YARN) {
+        auto pair_of = [&](double turns) {
+            return d * std::log(s.original / (turns * kTwoPi)) / (2.0 * std::log(base));
+        };
+        first = std::max(0.0, std::floor(pair_of(s.high)));
+        last = std::min(d - 1.0, std::ceil(pair_of(s.low)));
+    }
+    for (int64_t i = 0; i < rot_dim / 2; ++i) {
+        const double f = std::pow(b, -2.0 * static_cast<double>(i) / d);
+        double keep = 1.0;  // share of the unscaled frequency
+        if (s.kind == SS_ROPE_LINEAR) keep = 0.0;
+        if (s.kind == SS_ROPE_LLAMA3) {
+            const double turns = s.original * f / kTwoPi;  // over the original length
+            keep = std::min(1.0, std::max(0.0, (turns - s.low) / (s.high - s.low)));
+        }
+        if (s.kind == SS_ROPE_YARN)
+            keep = 1.0 - std::min(1.0, std::max(0.0, (static_cast<double>(i) - first) /
+                                                         std::max(last - first, 0.001)));
+        freqs[i] = f * (keep + (1.0 - keep) / (s.kind == SS_ROPE_NONE ? 1.0 : s.factor));
+    }
+    *scale = s.kind == SS_ROPE_YARN && s.factor > 1.0 ? 0.1 * std::log(s.factor) + 1.0 : 1.0;
+    return SS_OK;
+}
+
+ss_status ss_rope(const ss_rope_heads* q, const ss_rope_heads* k, ss_in_dtype dtype,
+                  const void* positions, int32_t positions64, const double* freqs, float scale,
+                  int64_t T, int64_t head_dim, int64_t rot_dim, ss_rope_layout layout,
+                  ss_stream_t stream) {
+    if (!q || !positions || !freqs || (positions64 != 0 && positions64 != 1))
+        return SS_ERR_INVALID_ARG;
+    if (dtype != SS_IN_F32 && dtype != SS_IN_BF16) return SS_ERR_INVALID_ARG;
+    if (layout != SS_ROPE_HALF && layout != SS_ROPE_INTERLEAVED) return SS_ERR_INVALID_ARG;
+    if (T <= 0 || T > INT32_MAX - ss::kRopeMaxTokens || head_dim < 2 || rot_dim < 2 ||
+        rot_dim % 2 != 0 || rot_dim > head_dim)
+        return SS_ERR_INVALID_ARG;
+    if (head_dim > ss::kRopeMaxDim) return SS_ERR_UNSUPPORTED;
+    const uintptr_t esz = dtype == SS_IN_F32 ? 4 : 2;
+    ss::RopeArgs a = {};
+    const ss_rope_heads* hs[2] = {q, k};
+    for (int i = 0; i < 2; ++i) {
+        if (!hs[i]) continue;
+        const ss_rope_heads& h = *hs[i];
+        if (!h.in || !h.out || h.heads <= 0 || h.heads > 65536) return SS_ERR_INVALID_ARG;
+        if (reinterpret_cast<uintptr_t>(h.in) % esz || reinterpret_cast<uintptr_t>(h.out) % esz)
+            return SS_ERR_ALIGNMENT;
+        a.t[i] = {h.in,      h.out,      static_cast<int>(h.heads), h.in_token,
+                  h.in_head, h.out_token, h.out_head};
+    }
+    if (reinterpret_cast<uintptr_t>(positions) % (positions64 ? 8 : 4) ||
+        reinterpret_cast<uintptr_t>(freqs) % 8)
+        return SS_ERR_ALIGNMENT;
+    int dev;
+    const ss_status st = check_device(&dev);
+    if (st != SS_OK) return st;
+    a.pos = positions;
+    a.pos64 = positions64;
+    a.freq = freqs;
+    a.scale = scale;
+    a.T = static_cast<int>(T);
+    a.D = static_cast<int>(head_dim);
+    a.rot = static_cast<int>(rot_dim);
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return dtype == SS_IN_BF16 ? dispatch_rope<__nv_bfloat16>(a, layout == SS_ROPE_HALF, s)
+                               : dispatch_rope<float>(a, layout == SS_ROPE_HALF, s);
+}
+
+ss_status ss_norm_quant_lift_act(const void* X, ss_in_dtype in_dtype, const void* weight,
+                                 ss_in_dtype weight_dtype, float eps, int64_t M, int64_t K,
+                                 ss_pattern p, ss_qdtype q, void* Xq_lift, float* s_x,
+                                 ss_stream_t stream) {
+    int64_t K_pad, K_lift, K_lp;
+    ss_status st = ss_slide_shape(p, K, &K_pad, &K_lift, &K_lp);
+    if (st != SS_OK) return st;
+    const int kq = kernel_q(q);
+    if (kq < 0) return SS_ERR_INVALID_ARG;
+    const bool scaled = kq != ss::kQBf16;  // the bf16 tier has no scale (s_x unused)
+    if (!X || !weight || !Xq_lift || (scaled && !s_x) || M <= 0 || M > INT32_MAX)
+        return SS_ERR_INVALID_ARG;
+    if ((in_dtype != SS_IN_F32 && in_dtype != SS_IN_BF16) ||
+        (weight_dtype != SS_IN_F32 && weight_dtype != SS_IN_BF16))
+        return SS_ERR_INVALID_ARG;
+    if (!(eps >= 0.0f) || !std::isfinite(eps)) return SS_ERR_INVALID_ARG;
+    if (!aligned16(X) || !aligned16(weight) || !aligned16(Xq_lift) || (scaled && !aligned16(s_x)))
+        return SS_ERR_ALIGNMENT;
+    int dev;
+    if ((st = check_device(&dev)) != SS_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int wf32 = weight_dtype == SS_IN_F32, Nh = p.group / 2;
+#define SS_NORM(T, Q) \
+    return launch_norm<T, Q>(X, weight, wf32, eps, M, K, Nh, K_lift, K_lp, Xq_lift, s_x, s)
+    if (in_dtype == SS_IN_BF16) {
+        if (kq == ss::kQInt8) SS_NORM(__nv_bfloat16, ss::kQInt8);
+        if (kq == ss::kQBf16) SS_NORM(__nv_bfloat16, ss::kQBf16);
+        SS_NORM(__nv_bfloat16, ss::kQE4M3);
+    }
+    if (kq == ss::kQInt8) SS_NORM(float, ss::kQInt8);
+    if (kq == ss::kQBf16) SS_NORM(float, ss::kQBf16);
+    SS_NORM(float, ss::kQE4M3);
+#undef SS_NORM
+}
+
+}  // extern "C"

@@ -44,6 +44,7 @@
 #include <type_traits>
 
 #include "ss_common.cuh"
+#include "ss_epilogue.cuh"
 
 namespace ss {
 
@@ -185,6 +186,7 @@ struct GemmArgs {
     const float* s_a;
     const float* s_b;
     void* y;
+    EpiArgs epi;      // the fused epilogue (kernels with kEpi)
 };
 
 template <bool kInt8, bool kOutBf16>
@@ -197,6 +199,51 @@ __device__ __forceinline__ void store_scaled(void* y, int64_t off, uint32_t acc_
         reinterpret_cast<__nv_bfloat16*>(y)[off] = __float2bfloat16_rn(v);
     else
         reinterpret_cast<float*>(y)[off] = v;
+}
+
+// Epilogue of one thread's accumulator row (a_row, columns b0 .. b0 + 31)
+// straight to global memory; sa is the row's scale, sb_lane the scale of
+// column b0 + lane.
+template <bool kInt8, bool kOutBf16>
+__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uint32_t (&r)[32],
+                                                 int a_row, int b0, int lane, float sa,
+                                                 float sb_lane) {
+    const EpiArgs& e = args.epi;
+    const bool row_ok = a_row < args.rowsA;
+    const float bias_row = args.a_is_w ? epi_bias(e, a_row, row_ok) : 0.0f;
+    const float bias_lane =
+        args.a_is_w ? 0.0f : epi_bias(e, b0 + lane, b0 + lane < args.rowsB);
+    float v[32];
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+        const float sb = __shfl_sync(0xffffffffu, sb_lane, u);
+        const float acc = kInt8 ? __int2float_rn(static_cast<int32_t>(r[u])) : __uint_as_float(r[u]);
+        const float d = args.a_is_w ? __fmul_rn(__fmul_rn(acc, sb), sa)
+                                    : __fmul_rn(__fmul_rn(acc, sa), sb);
+        v[u] = d + (args.a_is_w ? bias_row : __shfl_sync(0xffffffffu, bias_lane, u));
+    }
+#pragma unroll
+    for (int u = 0; u < 32; ++u) {
+        const int b_row = b0 + u;
+        float y;
+        int64_t off;
+        bool mine = row_ok && b_row < args.rowsB;
+        if (!e.gated) {
+            off = args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy + a_row
+                              : static_cast<int64_t>(a_row) * args.ldy + b_row;
+            y = activate(v[u], e.act);
+            if (e.residual && mine) y += epi_residual(e, off);
+        } else if (args.a_is_w) {  // the partner row is 8 lanes up
+            y = activate(v[u], e.act) * __shfl_down_sync(0xffffffffu, v[u], 8);
+            off = static_cast<int64_t>(b_row) * args.ldy + gated_col(a_row);
+            mine = mine && (a_row & 8) == 0;
+        } else {  // the partner column is this thread's
+            if (u & 8) continue;
+            y = activate(v[u], e.act) * v[(u + 8) & 31];
+            off = static_cast<int64_t>(a_row) * args.ldy + gated_col(b_row);
+        }
+        if (mine) store_y<kOutBf16>(args.y, off, y);
+    }
 }
 
 // Output tile t -> (A tile ta, B tile tb).  Consecutive tiles (the ones a
@@ -239,8 +286,9 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
 
 // kQ: kQE4M3, kQInt8 (kind::f8f6f4 / kind::i8), kQBf16 (kind::f16) or kQNvfp4
 // (kind::mxf4nvf4, block-scaled; tm_sfa / tm_sfb are its scale-factor maps,
-// unused otherwise, and s_a is one global scale).
-template <bool kSparse, int kQ, bool kOutBf16, int kPair>
+// unused otherwise, and s_a is one global scale).  kEpi: the fused epilogue of
+// args.epi (ss_epilogue.cuh).
+template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_e, const __grid_constant__ CUtensorMap tm_y,
@@ -610,7 +658,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const float sa = kFp4 ? __ldg(args.s_a) : load_scale<kBf16>(args.s_a, a_row, row_ok);
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
-            if (args.tma_store && args.a_is_w) {
+            if (!kEpi && args.tma_store && args.a_is_w) {
                 // Transposed store path.  Each warp reads its 32 channels x 32
                 // tokens of a chunk as m8n8 fragments (two 16-lane halves),
                 // scales them, packs bf16 pairs and writes 8x8 blocks with
@@ -754,7 +802,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             mbar_arrive(&acc_empty[acc]);
                     }
                 }
-                if (args.tma_store) {
+                if constexpr (kEpi) {
+                    epi_store_direct<kInt8, kOutBf16>(args, r, a_row, b0 + c, lane, sa, sb_lane);
+                } else if (args.tma_store) {
                     if (issuer) bulk_wait_read<0>();  // the group's last store has read it
                     named_bar_sync(grp_bar, 128);
                     if (args.a_is_w) {

@@ -60,8 +60,9 @@ struct SplitKCfg {
 };
 
 // args.k_stages: stages of the whole K; args.bn: B rows (a multiple of 32,
-// <= kSkBn, covering every B row); args.a_is_w must be 1.
-template <bool kSparse, int kQ, bool kOutBf16>
+// <= kSkBn, covering every B row); args.a_is_w must be 1.  kEpi: the fused
+// epilogue of args.epi (ss_epilogue.cuh).
+template <bool kSparse, int kQ, bool kOutBf16, bool kEpi = false>
 __global__ void __launch_bounds__(kSplitKThreads, 1)
     gemm_splitk_kernel(const __grid_constant__ CUtensorMap tm_a,
                        const __grid_constant__ CUtensorMap tm_b,
@@ -254,11 +255,8 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
         const int et = threadIdx.x - 64;  // 0..127
         uint32_t peer[8];
         for (int p = 0; p < S; ++p) peer[p] = map_to_rank(part, static_cast<uint32_t>(p));
-        for (int f = et; f < rows * args.bn; f += 128) {
-            const int rl = f % rows, col = f / rows;
-            const int ch = a0 + r0 + rl;  // A row = output channel
-            const int tok = col;          // B row = token
-            if (ch >= args.rowsA || tok >= args.rowsB) continue;
+        // the dequantised sum of the parts at (row rl of this slice, column col)
+        auto dequant = [&](int rl, int col) {
             const uint32_t off = static_cast<uint32_t>((col * kTileA + r0 + rl) * 4);
             float accv;
             if constexpr (kInt8) {
@@ -277,14 +275,35 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
                     accv = __fadd_rn(accv, __uint_as_float(v));
                 }
             }
-            const float sa = load_scale<kBf16>(args.s_a, ch, true);
-            const float sb = load_scale<kBf16>(args.s_b, tok, true);
-            const float y = __fmul_rn(__fmul_rn(accv, sb), sa);
-            const int64_t o = static_cast<int64_t>(tok) * args.ldy + ch;
-            if constexpr (kOutBf16)
-                reinterpret_cast<__nv_bfloat16*>(args.y)[o] = __float2bfloat16_rn(y);
-            else
-                reinterpret_cast<float*>(args.y)[o] = y;
+            const float sa = load_scale<kBf16>(args.s_a, a0 + r0 + rl, true);
+            const float sb = load_scale<kBf16>(args.s_b, col, true);
+            return __fmul_rn(__fmul_rn(accv, sb), sa);
+        };
+        if (kEpi && args.epi.gated) {  // a slice is whole 16-row groups: both factors are here
+            for (int f = et; f < rows / 2 * args.bn; f += 128) {
+                const int i = f % (rows / 2), col = f / (rows / 2);
+                const int rl = ((i >> 3) << 4) | (i & 7);
+                const int ch = a0 + r0 + rl;
+                if (ch >= args.rowsA || col >= args.rowsB) continue;
+                const float g = dequant(rl, col) + epi_bias(args.epi, ch, true);
+                const float u = dequant(rl + 8, col) + epi_bias(args.epi, ch + 8, true);
+                store_y<kOutBf16>(args.y, static_cast<int64_t>(col) * args.ldy + gated_col(ch),
+                                  activate(g, args.epi.act) * u);
+            }
+        } else {
+            for (int f = et; f < rows * args.bn; f += 128) {
+                const int rl = f % rows, col = f / rows;
+                const int ch = a0 + r0 + rl;  // A row = output channel
+                const int tok = col;          // B row = token
+                if (ch >= args.rowsA || tok >= args.rowsB) continue;
+                float y = dequant(rl, col);
+                const int64_t o = static_cast<int64_t>(tok) * args.ldy + ch;
+                if constexpr (kEpi) {
+                    y = activate(y + epi_bias(args.epi, ch, true), args.epi.act);
+                    if (args.epi.residual) y += epi_residual(args.epi, o);
+                }
+                store_y<kOutBf16>(args.y, o, y);
+            }
         }
     }
     cluster_sync_all();  // no CTA leaves while a peer may still read its partials
