@@ -320,8 +320,10 @@ ss_status ss_dense_gemm_nvfp4_fused(const void *Xv, const void *Xs, const float 
  *   y[k] = X[m, k] * rsqrt(mean_k X[m, k]^2 + eps) * weight[k]
  * then as ss_quant_lift_act on y, which is never written or rounded itself
  * (SS_BF16: rounded to bf16 as it is stored).  weight is [K], bf16 or fp32
- * whatever X's type; eps >= 0.  Rows must be finite, with a sum of squares
- * below the fp32 range; a row with max|y| < 1e-35 has codes 0 and s_x 0. */
+ * whatever X's type; eps >= 0.  The codes are those of z = X * weight (the
+ * row's factor cancels): for bf16 X and weight exactly RNE(Q z / max|z|).
+ * Rows must be finite, with a sum of squares below the fp32 range and max|z|
+ * below 2^119; a row with max|z| < 1e-35 has codes 0 and s_x 0. */
 ss_status ss_norm_quant_lift_act(const void *X, ss_in_dtype in_dtype, const void *weight,
                                  ss_in_dtype weight_dtype, float eps, int64_t M, int64_t K,
                                  ss_pattern p, ss_qdtype q, void *Xq_lift, float *s_x,

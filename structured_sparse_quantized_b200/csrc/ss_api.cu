@@ -150,7 +150,7 @@ bool make_map_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
 // box [32 tokens][128 channels] when A rows are channels, [128 tokens][32
 // channels] otherwise.  Returns false (direct stores instead) when the rows
 // of Y are not 16-byte aligned.
-bool make_y_map(CUtensorMap* map, void* Y, int64_t M, int64_t N, bool out_bf16, bool a_is_w) {
+bool make_y_map(CUtensorMap* map, const void* Y, int64_t M, int64_t N, bool out_bf16, bool a_is_w) {
     const uint32_t esz = out_bf16 ? 2 : 4;
     if (!out_bf16 || (N * esz) % 16 != 0) return false;  // fp32 Y: direct stores
     const CUtensorMapDataType dt =
@@ -164,10 +164,11 @@ bool make_y_map(CUtensorMap* map, void* Y, int64_t M, int64_t N, bool out_bf16, 
 
 template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi>
 ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& e,
-                      const CUtensorMap& y, const ss::GemmArgs& args, cudaStream_t stream,
-                      const CUtensorMap* sfa = nullptr, const CUtensorMap* sfb = nullptr) {
-    using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair>,
-                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1>>;
+                      const CUtensorMap& y, const CUtensorMap& r, const ss::GemmArgs& args,
+                      cudaStream_t stream, const CUtensorMap* sfa = nullptr,
+                      const CUtensorMap* sfb = nullptr) {
+    using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair, kEpi>,
+                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi>>;
     auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
@@ -182,34 +183,52 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
     const int64_t units = g_num_sms[dev] / kPair;
     const int grid = static_cast<int>((tiles < units ? tiles : units) * kPair);
     return launch_ex(kern, dim3(grid), dim3(ss::kGemmThreads), C::kSmemBytes, stream, kPair, a, b,
-                     e, y, sfa ? *sfa : a, sfb ? *sfb : a, args);
+                     e, y, sfa ? *sfa : a, sfb ? *sfb : a, r, args);
 }
 
 // q: ss::kQE4M3, kQInt8 or kQBf16; bf16: Y element type.
 template <bool kSparse, int kPair, bool kEpi>
 ss_status dispatch_gemm(int dev, int q, bool bf16, const CUtensorMap& a, const CUtensorMap& b,
-                        const CUtensorMap& e, const CUtensorMap& y, const ss::GemmArgs& args,
-                        cudaStream_t st) {
+                        const CUtensorMap& e, const CUtensorMap& y, const CUtensorMap& r,
+                        const ss::GemmArgs& args, cudaStream_t st) {
     using namespace ss;
     if (q == kQInt8)
-        return bf16 ? launch_gemm<kSparse, kQInt8, true, kPair, kEpi>(dev, a, b, e, y, args, st)
-                    : launch_gemm<kSparse, kQInt8, false, kPair, kEpi>(dev, a, b, e, y, args, st);
+        return bf16 ? launch_gemm<kSparse, kQInt8, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
+                    : launch_gemm<kSparse, kQInt8, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
     if (q == kQBf16)
-        return bf16 ? launch_gemm<kSparse, kQBf16, true, kPair, kEpi>(dev, a, b, e, y, args, st)
-                    : launch_gemm<kSparse, kQBf16, false, kPair, kEpi>(dev, a, b, e, y, args, st);
-    return bf16 ? launch_gemm<kSparse, kQE4M3, true, kPair, kEpi>(dev, a, b, e, y, args, st)
-                : launch_gemm<kSparse, kQE4M3, false, kPair, kEpi>(dev, a, b, e, y, args, st);
+        return bf16 ? launch_gemm<kSparse, kQBf16, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
+                    : launch_gemm<kSparse, kQBf16, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
+    return bf16 ? launch_gemm<kSparse, kQE4M3, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
+                : launch_gemm<kSparse, kQE4M3, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
 }
 
 template <bool kSparse>
 ss_status dispatch_gemm_any(int dev, int q, bool bf16, int pair, bool fused, const CUtensorMap& a,
                             const CUtensorMap& b, const CUtensorMap& e, const CUtensorMap& y,
-                            const ss::GemmArgs& args, cudaStream_t st) {
+                            const CUtensorMap& r, const ss::GemmArgs& args, cudaStream_t st) {
     if (pair == 1)
-        return fused ? dispatch_gemm<kSparse, 1, true>(dev, q, bf16, a, b, e, y, args, st)
-                     : dispatch_gemm<kSparse, 1, false>(dev, q, bf16, a, b, e, y, args, st);
-    return fused ? dispatch_gemm<kSparse, 2, true>(dev, q, bf16, a, b, e, y, args, st)
-                 : dispatch_gemm<kSparse, 2, false>(dev, q, bf16, a, b, e, y, args, st);
+        return fused ? dispatch_gemm<kSparse, 1, true>(dev, q, bf16, a, b, e, y, r, args, st)
+                     : dispatch_gemm<kSparse, 1, false>(dev, q, bf16, a, b, e, y, r, args, st);
+    return fused ? dispatch_gemm<kSparse, 2, true>(dev, q, bf16, a, b, e, y, r, args, st)
+                 : dispatch_gemm<kSparse, 2, false>(dev, q, bf16, a, b, e, y, r, args, st);
+}
+
+// Maps and paths of Y and the residual (N columns of Y; A rows = channels or
+// not): sets args.tma_store and args.tma_res; unused maps are copies of `any`.
+void epilogue_maps(const CUtensorMap& any, void* Y, int64_t M, int64_t N, bool bf16, bool fused,
+                   ss::GemmArgs* args, CUtensorMap* y, CUtensorMap* r) {
+    *y = *r = any;
+    args->tma_res = 0;
+    args->tma_store = make_y_map(y, Y, M, N, bf16, args->a_is_w) ? 1 : 0;
+    if (!fused || !args->tma_store) return;
+    // a fused epilogue takes the TMA path for channel rows, unless the residual
+    // is fp32
+    if (!args->a_is_w || args->epi.res_f32) {
+        args->tma_store = 0;
+    } else if (args->epi.residual) {
+        args->tma_res = make_y_map(r, args->epi.residual, M, N, true, true) ? 1 : 0;
+        args->tma_store = args->tma_res;
+    }
 }
 
 // The fused epilogue `epi` of a product with N output channels, checked; with
@@ -580,10 +599,8 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
     args.s_a = s_a;
     args.s_b = s_b;
     args.y = Y;
-    CUtensorMap ty;
-    args.tma_store =
-        !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, args.a_is_w) ? 1 : 0;
-    if (!args.tma_store) ty = ta;  // unused
+    CUtensorMap ty, tr;
+    epilogue_maps(ta, Y, M, args.ldy, out_dtype == SS_OUT_BF16, fused, &args, &ty, &tr);
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool i8 = q == SS_INT8, bf = out_dtype == SS_OUT_BF16;
     const int forced = forced_sparse_kernel();
@@ -619,7 +636,7 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
                   : launch_gemm_wide<false, false>(dev, wa, wb, te, ty, wargs, st_);
     }
 #endif
-    return dispatch_gemm_any<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, args, st_);
+    return dispatch_gemm_any<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, tr, args, st_);
 }
 
 // ss_dense_gemm and ss_dense_gemm_fused.
@@ -662,9 +679,8 @@ ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const flo
     args.s_a = s_w;
     args.s_b = s_x;
     args.y = Y;
-    CUtensorMap ty;
-    args.tma_store = !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
-    if (!args.tma_store) ty = ta;  // unused
+    CUtensorMap ty, tr;
+    epilogue_maps(ta, Y, M, args.ldy, out_dtype == SS_OUT_BF16, fused, &args, &ty, &tr);
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = out_dtype == SS_OUT_BF16;
     if (forced_sparse_kernel() != 1) {  // decode sizes: split K over a cluster
@@ -673,7 +689,7 @@ ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const flo
             split(dev, kq, bf, N, M, Wq, K_p * eb, Xq, K_p * eb, ta, args, st_);
         if (sk != SS_ERR_UNSUPPORTED) return sk;
     }
-    return dispatch_gemm_any<false>(dev, kq, bf, pair, fused, ta, tb, ta, ty, args, st_);
+    return dispatch_gemm_any<false>(dev, kq, bf, pair, fused, ta, tb, ta, ty, tr, args, st_);
 }
 
 }  // namespace
@@ -803,15 +819,14 @@ ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float
     args.s_a = g_w;
     args.s_b = g_x;
     args.y = Y;
-    CUtensorMap ty;
-    args.tma_store = !fused && make_y_map(&ty, Y, M, N, out_dtype == SS_OUT_BF16, true) ? 1 : 0;
-    if (!args.tma_store) ty = ta;  // unused
+    CUtensorMap ty, tr;
+    epilogue_maps(ta, Y, M, args.ldy, out_dtype == SS_OUT_BF16, fused, &args, &ty, &tr);
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = out_dtype == SS_OUT_BF16;
 #define SS_FP4_GO(P, E)                                                                       \
-    return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, P, E>(dev, ta, tb, te, ty, args, st_, \
+    return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, P, E>(dev, ta, tb, te, ty, tr, args, st_, \
                                                               &tsa, &tsb)                     \
-              : launch_gemm<kSparse, ss::kQNvfp4, false, P, E>(dev, ta, tb, te, ty, args,     \
+              : launch_gemm<kSparse, ss::kQNvfp4, false, P, E>(dev, ta, tb, te, ty, tr, args, \
                                                                st_, &tsa, &tsb)
     if (pair == 2) {
         if (fused) SS_FP4_GO(2, true);

@@ -41,10 +41,42 @@ ss_status dispatch_rope(const ss::RopeArgs& a, bool half, cudaStream_t s) {
     return vec ? launch_rope<T, V, false>(a, s) : launch_rope<T, 1, false>(a, s);
 }
 
+template <typename T, int kQ, int kChunks, int kWpr>
+ss_status launch_norm_reg(const void* X, const void* w, int wf32, float eps, int64_t M, int64_t K,
+                          int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
+                          cudaStream_t s) {
+    constexpr int kRows = ss::kWarpRowThreads / (32 * kWpr);
+    // 4:6, 8:10: one row of codes per row slot, with a chunk past the last group
+    const int eb = kQ == ss::kQBf16 ? 2 : 1;
+    const int q_stride =
+        Nh == 3 || Nh == 5
+            ? static_cast<int>(round_up((K + 2 * Nh) * eb, 16) + round_up(16 * eb, 16) + 16)
+            : 0;
+    auto kern = ss::norm_quant_lift_reg_kernel<T, kQ, kChunks, kWpr>;
+    const size_t smem = static_cast<size_t>(kRows) * q_stride;
+    const ss_status st = set_smem(kern, 0, smem);
+    if (st != SS_OK) return st;
+    return launch_ex(kern, dim3(static_cast<unsigned>((M + kRows - 1) / kRows)),
+                     dim3(ss::kWarpRowThreads), smem, s, 1, static_cast<const T*>(X), w, wf32, eps,
+                     M, static_cast<int>(K), Nh, static_cast<int>(K_lift), static_cast<int>(K_lp),
+                     q_stride, static_cast<uint8_t*>(Xq), s_x);
+}
+
 template <typename T, int kQ>
-ss_status launch_norm(const void* X, const void* w, int wf32, float eps, int64_t M, int64_t K,
-                      int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
+ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps, int64_t M,
+                      int64_t K, int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
                       cudaStream_t s) {
+#define SS_NORM_REG(C, W)     return launch_norm_reg<T, kQ, C, W>(X, w, wf32, eps, M, K, Nh, K_lift, K_lp, Xq, s_x, s)
+    if (M <= g_num_sms[dev]) {  // few rows: eight warps to each
+        if (K <= 4096) SS_NORM_REG(1, 8);
+        if (K <= 8192) SS_NORM_REG(2, 8);
+    }
+    if (K <= 1024) SS_NORM_REG(2, 1);
+    if (K <= 2048) SS_NORM_REG(4, 1);
+    if (K <= 4096) SS_NORM_REG(4, 2);
+    if (K <= 8192) SS_NORM_REG(4, 4);
+    if (K <= 16384) SS_NORM_REG(4, 8);
+#undef SS_NORM_REG
     return launch_ex(ss::norm_quant_lift_kernel<T, kQ>, dim3(static_cast<unsigned>(M)),
                      dim3(ss::kWarpRowThreads), 0, s, 1, static_cast<const T*>(X), w, wf32, eps, M,
                      static_cast<int>(K), Nh, static_cast<int>(K_lift), static_cast<int>(K_lp),
@@ -163,7 +195,7 @@ ss_status ss_norm_quant_lift_act(const void* X, ss_in_dtype in_dtype, const void
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const int wf32 = weight_dtype == SS_IN_F32, Nh = p.group / 2;
 #define SS_NORM(T, Q) \
-    return launch_norm<T, Q>(X, weight, wf32, eps, M, K, Nh, K_lift, K_lp, Xq_lift, s_x, s)
+    return launch_norm<T, Q>(dev, X, weight, wf32, eps, M, K, Nh, K_lift, K_lp, Xq_lift, s_x, s)
     if (in_dtype == SS_IN_BF16) {
         if (kq == ss::kQInt8) SS_NORM(__nv_bfloat16, ss::kQInt8);
         if (kq == ss::kQBf16) SS_NORM(__nv_bfloat16, ss::kQBf16);

@@ -75,13 +75,55 @@ __device__ __forceinline__ float epi_bias(const EpiArgs& e, int ch, bool in_rang
 // The residual may be Y itself (same elements, read before they are written
 // by the same thread), so it is not read through the non-coherent path.
 __device__ __forceinline__ float epi_residual(const EpiArgs& e, int64_t off) {
-    return e.res_f32 ? static_cast<const volatile float*>(e.residual)[off]
-                     : __uint_as_float(static_cast<uint32_t>(
-                           static_cast<const volatile uint16_t*>(e.residual)[off]) << 16);
+    return e.res_f32 ? static_cast<const float*>(e.residual)[off]
+                     : __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[off]);
 }
 
 // Output column of weight row ch of a gated product (its gate rows).
 __device__ __forceinline__ int gated_col(int ch) { return ((ch >> 4) << 3) | (ch & 7); }
+
+// act on the fragment y[2][16] of a thread (see epi_tile_channels): every
+// value, or the gates (values 4 r + k).
+template <int kAct, bool kGates>
+__device__ __forceinline__ void activate_fragment(float (&y)[2][16]) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int j = 0; j < 16; ++j)
+            if (!kGates || (j & 2) == 0) y[h][j] = activate<kAct>(y[h][j]);
+}
+
+template <bool kGates>
+__device__ __forceinline__ void epi_activate(float (&y)[2][16], int act) {
+    switch (act) {
+        case kActRelu: activate_fragment<kActRelu, kGates>(y); break;
+        case kActSilu: activate_fragment<kActSilu, kGates>(y); break;
+        case kActGelu: activate_fragment<kActGelu, kGates>(y); break;
+        case kActGeluErf: activate_fragment<kActGeluErf, kGates>(y); break;
+        default: break;
+    }
+}
+__device__ __forceinline__ void epi_activate_all(float (&y)[2][16], int act) {
+    epi_activate<false>(y, act);
+}
+__device__ __forceinline__ void epi_activate_gates(float (&y)[2][16], int act) {
+    epi_activate<true>(y, act);
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Address of this thread's row of the four 8x8 blocks (r = 2 rp, 2 rp + 1) x
+// (channel blocks e = 0, 1) in a staged [2 halves][32 tokens][64 channels]
+// chunk with 128B swizzle.
+__device__ __forceinline__ uint32_t epi_block_addr(uint32_t base, int rp, int q, int h, int mi,
+                                                   int mj) {
+    const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
+    const int ch = q * 32 + 16 * h + 8 * (mi & 1);
+    return base + (ch >> 6) * (32 * 128) + tok * 128 + ((((ch & 63) >> 3) ^ (tok & 7)) << 4);
+}
 
 template <bool kOutBf16>
 __device__ __forceinline__ void store_y(void* y, int64_t off, float v) {

@@ -54,7 +54,7 @@ constexpr int kL2PrefetchStages = 16;  // weight stages a CTA prefetches before 
 constexpr int kTileA = 128;  // A rows per CTA per A tile
 constexpr int kTmemCols = 512;
 
-template <bool kSparse, int kPair, int kEb = 1>
+template <bool kSparse, int kPair, int kEb = 1, bool kEpi = false>
 struct GemmCfg {
     // One pipeline stage covers kStageK logical K: for 8-bit operands dense
     // 128 (4 MMAs of K=32) and sparse 256 (4 MMAs of K=64); for bf16 (kEb = 2
@@ -85,7 +85,11 @@ struct GemmCfg {
     static constexpr int kStageRaw = kEOffset + kEBytes;
     static constexpr int kStageBytes = (kStageRaw + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;      // one 32-column bf16 chunk of Y
-    static constexpr int kSmemBudget = 225 * 1024 - 1024 - 256 - 2 * kEpiBytes;
+    // staging buffers for Y chunks: one per epilogue group, or two where the
+    // fused epilogue loads the residual of the next chunk into the other one
+    static constexpr int kEpiBufs = kEpi ? 4 : 2;
+    static constexpr int kSmemBudget =
+        (kEpi ? 226 : 225) * 1024 - 1024 - 256 - kEpiBufs * kEpiBytes;
     static constexpr int kStagesRaw = kSmemBudget / kStageBytes;
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
     static constexpr int kAccBufs = 2;                     // accumulators in TMEM
@@ -96,16 +100,16 @@ struct GemmCfg {
     // one metadata slot per stage: a slot is rewritten only after its stage's
     // "empty" commit, i.e. after the MMAs that read it completed
     static constexpr int kESlots = kStages;
-    static constexpr int kEpiOffset = kStages * kStageBytes;  // 2 staging buffers for Y chunks
+    static constexpr int kEpiOffset = kStages * kStageBytes;
     static constexpr int kSmemBytes =
-        kEpiOffset + 2 * kEpiBytes + 1024 /*align*/ + 256 /*barriers*/;
+        kEpiOffset + kEpiBufs * kEpiBytes + 1024 /*align*/ + 256 /*barriers*/;
     static_assert(kABytes % 1024 == 0 && kBAtomBytes % 1024 == 0, "tile alignment");
     static_assert(kARowBytes == 128 && kMmaPerStage == 4, "stage geometry");
     static_assert(!kSparse || kECol + kESlots * kESlotCols <= kTmemCols, "TMEM budget");
     static_assert(kECol % 2 == 0 && kESlotCols % 2 == 0, "metadata column pairs stay aligned");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
     static_assert(kStages >= (kPair == 2 ? 3 : 2), "pipeline depth");
-    static_assert((2 * kStages + 5) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 9) * 8 + 4 <= 256, "barrier area");
 };
 
 // Stage layout of the block-scaled FP4 GEMM: per stage 4 MMAs (sparse: K =
@@ -123,7 +127,7 @@ struct GemmCfg {
 // After the accumulators, tensor memory holds per stage a metadata slot (8
 // columns, sparse) and a scale slot (4 columns per MMA for A, 4 per MMA and
 // scale tile for B).
-template <bool kSparse, int kPair = 1>
+template <bool kSparse, int kPair = 1, bool kEpi = false>
 struct Fp4Cfg {
     static constexpr int kStageK = kSparse ? 512 : 256;
     static constexpr int kMmaK = kSparse ? 128 : 64;
@@ -149,7 +153,9 @@ struct Fp4Cfg {
     static constexpr int kSfbOffset = kSfaOffset + kSfaBytes;
     static constexpr int kStageBytes = (kSfbOffset + kSfbBytes + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;
-    static constexpr int kSmemBudget = 225 * 1024 - 1024 - 256 - 2 * kEpiBytes;
+    static constexpr int kEpiBufs = kEpi ? 4 : 2;
+    static constexpr int kSmemBudget =
+        (kEpi ? 226 : 225) * 1024 - 1024 - 256 - kEpiBufs * kEpiBytes;
     static constexpr int kStagesRaw = kSmemBudget / kStageBytes;
     static constexpr int kESlotCols = 4 * kEChunks;
     static constexpr int kSfaCols = 4 * kMmaPerStage;
@@ -164,10 +170,10 @@ struct Fp4Cfg {
     static constexpr int kESlots = kStages;
     static constexpr int kSfCol = kECol + kStages * kESlotCols;  // scale slots
     static constexpr int kEpiOffset = kStages * kStageBytes;
-    static constexpr int kSmemBytes = kEpiOffset + 2 * kEpiBytes + 1024 + 256;
+    static constexpr int kSmemBytes = kEpiOffset + kEpiBufs * kEpiBytes + 1024 + 256;
     static_assert(kSfCol % 4 == 0 && kSfCol + kSfSlotCols * kStages <= kTmemCols, "TMEM budget");
     static_assert(kSmemBytes <= 227 * 1024 && kStages >= 3, "shared memory budget");
-    static_assert((2 * kStages + 5) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 9) * 8 + 4 <= 256, "barrier area");
 };
 
 struct GemmArgs {
@@ -177,6 +183,8 @@ struct GemmArgs {
     int bn;           // B rows per tile (MMA N; multiple of 32, <= kBnMax)
     int a_is_w;       // 1: A rows are output channels (Y[b, a]); 0: Y[a, b]
     int ldy;          // leading dimension of Y (= N)
+    int tma_res;      // 1: the residual is bf16 and comes by TMA through the staging
+                      //    buffers (kEpi, with tma_store and a_is_w)
     int tma_store;    // 1: Y written by TMA tensor stores through shared memory
                       //    (A rows = channels: 128B-swizzled [32][64] halves)
     int e_chunks;     // K_lp / 128: 2 KB metadata tiles per 128 rows (tile-major)
@@ -222,27 +230,40 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uin
                                     : __fmul_rn(__fmul_rn(acc, sa), sb);
         v[u] = d + (args.a_is_w ? bias_row : __shfl_sync(0xffffffffu, bias_lane, u));
     }
+    const int64_t row0 = args.a_is_w ? a_row : static_cast<int64_t>(a_row) * args.ldy;
+    if (!e.gated) {
+        float res[32];  // every load is issued before the first store
 #pragma unroll
-    for (int u = 0; u < 32; ++u) {
-        const int b_row = b0 + u;
-        float y;
-        int64_t off;
-        bool mine = row_ok && b_row < args.rowsB;
-        if (!e.gated) {
-            off = args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy + a_row
-                              : static_cast<int64_t>(a_row) * args.ldy + b_row;
-            y = activate(v[u], e.act);
-            if (e.residual && mine) y += epi_residual(e, off);
-        } else if (args.a_is_w) {  // the partner row is 8 lanes up
-            y = activate(v[u], e.act) * __shfl_down_sync(0xffffffffu, v[u], 8);
-            off = static_cast<int64_t>(b_row) * args.ldy + gated_col(a_row);
-            mine = mine && (a_row & 8) == 0;
-        } else {  // the partner column is this thread's
-            if (u & 8) continue;
-            y = activate(v[u], e.act) * v[(u + 8) & 31];
-            off = static_cast<int64_t>(a_row) * args.ldy + gated_col(b_row);
+        for (int u = 0; u < 32; ++u) {
+            const int b_row = b0 + u;
+            const int64_t off = row0 + (args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy : b_row);
+            res[u] = e.residual && row_ok && b_row < args.rowsB ? epi_residual(e, off) : 0.0f;
         }
-        if (mine) store_y<kOutBf16>(args.y, off, y);
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            const int b_row = b0 + u;
+            const int64_t off = row0 + (args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy : b_row);
+            float y = activate(v[u], e.act);
+            if (e.residual) y += res[u];
+            if (row_ok && b_row < args.rowsB) store_y<kOutBf16>(args.y, off, y);
+        }
+    } else if (args.a_is_w) {  // the partner row is 8 lanes up
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            const int b_row = b0 + u;
+            const float y = activate(v[u], e.act) * __shfl_down_sync(0xffffffffu, v[u], 8);
+            if (row_ok && (a_row & 8) == 0 && b_row < args.rowsB)
+                store_y<kOutBf16>(
+                    args.y, static_cast<int64_t>(b_row) * args.ldy + gated_col(a_row), y);
+        }
+    } else {  // the partner column is this thread's
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+            const int b_row = b0 + u;
+            if ((u & 8) == 0 && row_ok && b_row < args.rowsB)
+                store_y<kOutBf16>(args.y, row0 + gated_col(b_row),
+                                  activate(v[u], e.act) * v[(u + 8) & 31]);
+        }
     }
 }
 
@@ -284,29 +305,213 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
     else return load_scale<kQ == kQBf16>(s, i, in_range);
 }
 
+// The fused epilogue of one output tile for one group of four warps, A rows =
+// channels and bf16 Y by TMA: the transposed store path of gemm_kernel with
+// bias, activation and residual between the scaling and the rounding.
+//
+// A thread's 16x256b fragments are channels q 32 + 16 h + 8 e + lane / 4 of
+// tokens 8 r + 2 (lane % 4) + k: the two factors of a gated output (8 channels
+// apart) are its e = 0 and e = 1, and the product leaves 16 channels per warp,
+// one 64-channel box per chunk instead of two.
+//
+// The residual chunk comes by TMA into the staging buffer that the chunk of Y
+// leaves from, in the same swizzled layout: ldmatrix.trans gives a thread the
+// elements that its stmatrix.trans then overwrites, so nothing else is staged
+// and Y may be the residual.  The buffers alternate: while a chunk is worked
+// on, the next chunk's residual (of the next tile after the last) lands in the
+// other buffer, so that its latency is hidden by a whole chunk, or by the wait
+// for the next accumulator.
+//
+// n: chunks this group has processed; issued: residual loads issued.  release
+// gives the accumulator back (one lane).  Returns false when a bounded wait
+// ran out (all four warps alike).
+template <typename C, int kQ, int kPair, typename Release>
+__device__ __forceinline__ bool epi_tile_channels(
+    const GemmArgs& args, const CUtensorMap& tm_y, const CUtensorMap& tm_r, uint8_t* stage,
+    uint64_t* res_full, volatile int* abort_flag, uint32_t& n, uint32_t& issued, int unit,
+    int n_units, int n_tiles, int nA, int nB, int tile_a_rows, int a_cta0, int b0, int grp, int q,
+    int lane, bool issuer, uint32_t t_row, Release release) {
+    constexpr bool kInt8 = kQ == kQInt8;
+    const EpiArgs& e = args.epi;
+    const uint32_t grp_bar = 1 + static_cast<uint32_t>(grp);
+    const int t4 = lane >> 2, tm = lane & 3;
+    const int mi = lane >> 3, mj = lane & 7;  // this thread's stmatrix matrix / row
+    // residual load of this group's chunk number j into buffer j & 1
+    const int per_tile = (args.bn - 32 * grp + 63) / 64;
+    auto load_residual = [&](uint32_t j) {
+        const int tile = unit + static_cast<int>(j / per_tile) * n_units;
+        if (tile >= n_tiles) return;
+        int ta, tb;
+        tile_coords(tile, nA, nB, args.a_groups, ta, tb);
+        const int ch = ta * tile_a_rows + a_cta0 % tile_a_rows;
+        const int tok = tb * args.bn + 32 * grp + 64 * static_cast<int>(j % per_tile);
+        uint8_t* dst = stage + (j & 1) * C::kEpiBytes;
+        mbar_arrive_expect_tx(&res_full[j & 1], C::kEpiBytes);
+        tma_load_2d(dst, &tm_r, &res_full[j & 1], ch, tok);
+        tma_load_2d(dst + 32 * 128, &tm_r, &res_full[j & 1], ch + 64, tok);
+        issued = j + 1;
+    };
+    if (args.tma_res && issuer && n == 0) load_residual(0);
+    float sa2[2][2], bias2[2][2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const int ch = a_cta0 + q * 32 + 16 * h + t4 + 8 * x;
+            sa2[h][x] = kQ == kQNvfp4 ? __ldg(args.s_a)
+                                      : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
+            bias2[h][x] = epi_bias(e, ch, ch < args.rowsA);
+        }
+    // One accumulator: read the group's whole part before any of it is worked
+    // on, so that the next tile's MMAs can start.  Two: chunk by chunk.
+    constexpr int kCpg = (C::kBnMax + 63) / 64;
+    constexpr int kBatch = C::kAccBufs == 1 ? kCpg : 1;
+#pragma unroll 1
+    for (int cb = 0; cb < kCpg; cb += kBatch) {
+        uint32_t v[kBatch][2][16];
+#pragma unroll
+        for (int cc = 0; cc < kBatch; ++cc) {
+            const int c = 32 * grp + 64 * (cb + cc);
+            if (c < args.bn) {
+                tmem_ld_16x256b_x4(t_row + c, v[cc][0]);
+                tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[cc][1]);
+            }
+        }
+        tmem_ld_wait();
+        if (32 * grp + 64 * cb >= args.bn) break;
+        if (32 * grp + 64 * (cb + kBatch) >= args.bn) {  // last read: release
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) release();
+        }
+#pragma unroll
+        for (int cc = 0; cc < kBatch; ++cc) {
+            const int c = 32 * grp + 64 * (cb + cc);
+            if (c >= args.bn) break;
+            uint8_t* buf = stage + (n & 1) * C::kEpiBytes;
+            const uint32_t sy = smem_u32(buf);
+            if (args.tma_res && issuer) {
+                bulk_wait_read<0>();  // the previous chunk has left the other buffer
+                load_residual(n + 1);
+            }
+            float y[2][16];  // [h][4 r + 2 x + k]
+            float sb[4][2];
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int tok = b0 + c + 8 * r + 2 * tm + k;
+                    sb[r][k] = load_b_scale<kQ>(args.s_b, tok, tok < args.rowsB);
+                }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 16; ++j) {
+                    const uint32_t bits = v[cc][h][j];
+                    const float acc =
+                        kInt8 ? __int2float_rn(static_cast<int32_t>(bits)) : __uint_as_float(bits);
+                    const int x = (j >> 1) & 1;
+                    y[h][j] = __fmul_rn(__fmul_rn(acc, sb[j >> 2][j & 1]), sa2[h][x]) + bias2[h][x];
+                }
+            uint32_t pk[2][8];
+            bool got = true;
+            if (e.gated) {
+                epi_activate_gates(y, e.act);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        pk[h][r] = pack_bf16(y[h][4 * r] * y[h][4 * r + 2],
+                                             y[h][4 * r + 1] * y[h][4 * r + 3]);
+            } else {
+                epi_activate_all(y, e.act);
+                if (args.tma_res) {
+                    got = mbar_wait(&res_full[n & 1], (n >> 1) & 1, abort_flag);
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int rp = 0; rp < 2; ++rp) {
+                        uint32_t rr[4] = {0u, 0u, 0u, 0u};
+                        if (args.tma_res)
+                            ldmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), rr);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int i = 8 * rp + 2 * j;
+                            float y0 = y[h][i], y1 = y[h][i + 1];
+                            if (args.tma_res) {
+                                y0 += __uint_as_float(rr[j] << 16);
+                                y1 += __uint_as_float(rr[j] & 0xFFFF0000u);
+                            }
+                            pk[h][4 * rp + j] = pack_bf16(y0, y1);
+                        }
+                    }
+            }
+            if (!args.tma_res) {  // the store of two chunks ago has left this buffer
+                if (issuer) bulk_wait_read<1>();
+                named_bar_sync(grp_bar, 128);
+            }
+            if (e.gated) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3
+                    stmatrix_x4_trans(sy + tok * 128 + (((2 * q + h) ^ (tok & 7)) << 4), pk[h][0],
+                                      pk[h][1], pk[h][2], pk[h][3]);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int rp = 0; rp < 2; ++rp)
+                        stmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), pk[h][4 * rp],
+                                          pk[h][4 * rp + 1], pk[h][4 * rp + 2],
+                                          pk[h][4 * rp + 3]);
+            }
+            fence_async_shared();
+            if (!named_bar_and(grp_bar, 128, got)) return false;
+            if (issuer) {
+                const uint64_t stream = l2_policy_evict_first();
+                if (e.gated) {
+                    tma_store_2d_hint(&tm_y, buf, a_cta0 / 2, b0 + c, stream);
+                } else {
+                    tma_store_2d_hint(&tm_y, buf, a_cta0, b0 + c, stream);
+                    tma_store_2d_hint(&tm_y, buf + 32 * 128, a_cta0 + 64, b0 + c, stream);
+                }
+                bulk_commit_group();
+            }
+            ++n;
+        }
+    }
+    return true;
+}
+
 // kQ: kQE4M3, kQInt8 (kind::f8f6f4 / kind::i8), kQBf16 (kind::f16) or kQNvfp4
 // (kind::mxf4nvf4, block-scaled; tm_sfa / tm_sfb are its scale-factor maps,
 // unused otherwise, and s_a is one global scale).  kEpi: the fused epilogue of
-// args.epi (ss_epilogue.cuh).
+// args.epi (ss_epilogue.cuh; tm_r is the residual's map, shaped as Y's).
 template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi = false>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_e, const __grid_constant__ CUtensorMap tm_y,
                 const __grid_constant__ CUtensorMap tm_sfa,
-                const __grid_constant__ CUtensorMap tm_sfb, const GemmArgs args) {
+                const __grid_constant__ CUtensorMap tm_sfb,
+                const __grid_constant__ CUtensorMap tm_r, const GemmArgs args) {
     constexpr bool kInt8 = kQ == kQInt8;
     constexpr bool kBf16 = kQ == kQBf16;
     constexpr bool kFp4 = kQ == kQNvfp4;
-    using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair>, GemmCfg<kSparse, kPair, kBf16 ? 2 : 1>>;
+    using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi>,
+                                 GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi>>;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kEpiOffset + 2 * C::kEpiBytes);
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + C::kEpiOffset + C::kEpiBufs * C::kEpiBytes);
     uint64_t* empty = full + C::kStages;
     uint64_t* acc_full = empty + C::kStages;  // [2]: one per accumulator buffer
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* res_full = drain + 1;  // [2 groups][2 buffers]: a chunk's residual has landed (kEpi)
+    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(res_full + 4);
     __shared__ int abort_flag_storage;
     volatile int* abort_flag = &abort_flag_storage;
     pdl_trigger();
@@ -335,6 +540,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             mbar_init(&acc_empty[b], kGemmEpiWarps * kPair);
         }
         mbar_init(drain, 1);
+        for (int b = 0; b < 4; ++b) mbar_init(&res_full[b], 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -624,9 +830,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const bool issuer = (ew & 3) == 0 && lane == 0;
         const uint32_t acc_empty_leader = kPair == 2 ? map_to_rank(acc_empty, 0) : 0u;
         constexpr int kEsz = 2;  // TMA-store staging is used for bf16 output only
-        uint8_t* sy = smem + C::kEpiOffset + grp * C::kEpiBytes;
+        uint8_t* sy = smem + C::kEpiOffset + grp * (C::kEpiBufs / 2) * C::kEpiBytes;
         int i = 0;
         bool ok = true;
+        uint32_t epi_n = 0, epi_issued = 0;  // chunks processed, residual loads issued (kEpi)
         for (int t = unit; t < n_tiles && ok; t += n_units, ++i) {
             int ta, tb;
             tile_coords(t, nA, nB, args.a_groups, ta, tb);
@@ -658,6 +865,22 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const float sa = kFp4 ? __ldg(args.s_a) : load_scale<kBf16>(args.s_a, a_row, row_ok);
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
+            if constexpr (kEpi && kOutBf16) {
+                if (args.tma_store && args.a_is_w) {
+                    // as the path below, with the fused epilogue
+                    if (!epi_tile_channels<C, kQ, kPair>(
+                            args, tm_y, tm_r, sy, &res_full[2 * grp], abort_flag, epi_n, epi_issued,
+                            unit, n_units, n_tiles, nA, nB, tile_a_rows, a_cta0, b0, grp, q, lane,
+                            issuer, t_row, [&] {
+                                if constexpr (kPair == 2)
+                                    mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
+                                else
+                                    mbar_arrive(&acc_empty[acc]);
+                            }))
+                        ok = false;
+                    continue;
+                }
+            }
             if (!kEpi && args.tma_store && args.a_is_w) {
                 // Transposed store path.  Each warp reads its 32 channels x 32
                 // tokens of a chunk as m8n8 fragments (two 16-lane halves),
@@ -869,6 +1092,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                     }
                 }
             }
+        }
+        if constexpr (kEpi) {  // after a wait that ran out: residual loads in flight land
+            for (; issuer && epi_n < epi_issued; ++epi_n)
+                mbar_drain(&res_full[2 * grp + (epi_n & 1)], (epi_n >> 1) & 1);
         }
         if (issuer) bulk_wait_all();  // Y stores done reading shared memory
     }
