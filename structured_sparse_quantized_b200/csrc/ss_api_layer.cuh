@@ -41,41 +41,73 @@ ss_status dispatch_rope(const ss::RopeArgs& a, bool half, cudaStream_t s) {
     return vec ? launch_rope<T, V, false>(a, s) : launch_rope<T, 1, false>(a, s);
 }
 
+// Bytes of a set's row of codes: 4:6 and 8:10 only, with a chunk past the last group.
+int norm_code_row(const ss::NormShape& s, int eb) {
+    return s.Nh == 3 || s.Nh == 5
+               ? static_cast<int>(round_up((s.K + 2 * s.Nh) * eb, 16) + 16 * eb + 16)
+               : 0;
+}
+
 template <typename T, int kQ, int kChunks, int kWpr>
-ss_status launch_norm_reg(const void* X, const void* w, int wf32, float eps, int64_t M, int64_t K,
-                          int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
-                          cudaStream_t s) {
-    constexpr int kRows = ss::kWarpRowThreads / (32 * kWpr);
-    // 4:6, 8:10: one row of codes per row slot, with a chunk past the last group
-    const int eb = kQ == ss::kQBf16 ? 2 : 1;
-    const int q_stride =
-        Nh == 3 || Nh == 5
-            ? static_cast<int>(round_up((K + 2 * Nh) * eb, 16) + round_up(16 * eb, 16) + 16)
-            : 0;
+ss_status launch_norm_reg(const void* X, const void* w, int wf32, float eps, int64_t M,
+                          const ss::NormShape& shape, void* Xq, float* s_x, cudaStream_t s) {
+    constexpr int kSets = ss::kWarpRowThreads / (32 * kWpr);
+    const int q_stride = norm_code_row(shape, kQ == ss::kQBf16 ? 2 : 1);
     auto kern = ss::norm_quant_lift_reg_kernel<T, kQ, kChunks, kWpr>;
-    const size_t smem = static_cast<size_t>(kRows) * q_stride;
+    const size_t smem = static_cast<size_t>(kSets) * q_stride;
     const ss_status st = set_smem(kern, 0, smem);
     if (st != SS_OK) return st;
-    return launch_ex(kern, dim3(static_cast<unsigned>((M + kRows - 1) / kRows)),
+    return launch_ex(kern, dim3(static_cast<unsigned>((M + kSets - 1) / kSets)),
                      dim3(ss::kWarpRowThreads), smem, s, 1, static_cast<const T*>(X), w, wf32, eps,
-                     M, static_cast<int>(K), Nh, static_cast<int>(K_lift), static_cast<int>(K_lp),
-                     q_stride, static_cast<uint8_t*>(Xq), s_x);
+                     M, shape, q_stride, static_cast<uint8_t*>(Xq), s_x);
+}
+
+template <typename T, int kQ, int kChunks, int kWpr>
+ss_status launch_norm_stream(int dev, const void* X, const void* w, int wf32, float eps, int64_t M,
+                             const ss::NormShape& shape, void* Xq, float* s_x, cudaStream_t s) {
+    constexpr int64_t kSets = ss::kWarpRowThreads / (32 * kWpr);
+    const int q_stride = norm_code_row(shape, kQ == ss::kQBf16 ? 2 : 1);
+    const int slot = static_cast<int>(round_up(shape.K * static_cast<int64_t>(sizeof(T)), 128));
+    auto kern = ss::norm_quant_lift_stream_kernel<T, kQ, kChunks, kWpr>;
+    const size_t smem = static_cast<size_t>(kSets) * (ss::kNormSlots * slot + q_stride);
+    const ss_status st = set_smem(kern, dev, smem);
+    if (st != SS_OK) return st;
+    int per_sm = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, ss::kWarpRowThreads, smem) !=
+            cudaSuccess ||
+        per_sm < 1)
+        return SS_ERR_CUDA;
+    const int64_t ctas = std::min<int64_t>((M + kSets - 1) / kSets,
+                                           static_cast<int64_t>(per_sm) * g_num_sms[dev]);
+    return launch_ex(kern, dim3(static_cast<unsigned>(ctas)), dim3(ss::kWarpRowThreads), smem, s, 1,
+                     static_cast<const T*>(X), w, wf32, eps, M, shape, slot, q_stride,
+                     static_cast<uint8_t*>(Xq), s_x);
 }
 
 template <typename T, int kQ>
 ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps, int64_t M,
                       int64_t K, int Nh, int64_t K_lift, int64_t K_lp, void* Xq, float* s_x,
                       cudaStream_t s) {
-#define SS_NORM_REG(C, W)     return launch_norm_reg<T, kQ, C, W>(X, w, wf32, eps, M, K, Nh, K_lift, K_lp, Xq, s_x, s)
-    if (M <= g_num_sms[dev]) {  // few rows: eight warps to each
-        if (K <= 4096) SS_NORM_REG(1, 8);
-        if (K <= 8192) SS_NORM_REG(2, 8);
+    const ss::NormShape shape = {static_cast<int>(K), Nh, static_cast<int>(K_lift),
+                                 static_cast<int>(K_lp), static_cast<int>((K + 15) / 16)};
+#define SS_NORM_REG(C, W) return launch_norm_reg<T, kQ, C, W>(X, w, wf32, eps, M, shape, Xq, s_x, s)
+#define SS_NORM_STREAM(C, W) \
+    return launch_norm_stream<T, kQ, C, W>(dev, X, w, wf32, eps, M, shape, Xq, s_x, s)
+    const bool stream = K * static_cast<int64_t>(sizeof(T)) % 16 == 0 &&
+                        M >= 8 * static_cast<int64_t>(g_num_sms[dev]);
+    if (stream) {
+        if (K <= 512) SS_NORM_STREAM(1, 1);
+        if (K <= 1024) SS_NORM_STREAM(1, 2);
+        if (K <= 2048) SS_NORM_STREAM(1, 4);
+        if (K <= 4096) SS_NORM_STREAM(1, 8);
+        if (K <= 8192) SS_NORM_STREAM(2, 8);
     }
-    if (K <= 1024) SS_NORM_REG(2, 1);
-    if (K <= 2048) SS_NORM_REG(4, 1);
-    if (K <= 4096) SS_NORM_REG(4, 2);
-    if (K <= 8192) SS_NORM_REG(4, 4);
+    if (K <= 512) SS_NORM_REG(1, 1);
+    if (K <= 2048) SS_NORM_REG(1, 4);
+    if (K <= 4096) SS_NORM_REG(1, 8);
+    if (K <= 8192) SS_NORM_REG(2, 8);
     if (K <= 16384) SS_NORM_REG(4, 8);
+#undef SS_NORM_STREAM
 #undef SS_NORM_REG
     return launch_ex(ss::norm_quant_lift_kernel<T, kQ>, dim3(static_cast<unsigned>(M)),
                      dim3(ss::kWarpRowThreads), 0, s, 1, static_cast<const T*>(X), w, wf32, eps, M,

@@ -710,6 +710,32 @@ __device__ __forceinline__ void mul_rn_f32x2(float a0, float a1, float b0, float
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
 }
 
+// Two fp32 multiply-adds in one instruction: (a0 * b0 + c0, a1 * b1 + c1),
+// each rounded once.
+__device__ __forceinline__ void fma_rn_f32x2(float a0, float a1, float b0, float b1, float c0,
+                                             float c1, float& r0, float& r1) {
+    uint64_t a, b, c, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(c) : "f"(c0), "f"(c1));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+}
+
+// max(a, |b|, |c|) for a >= 0; NaN operands are passed over.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest |v| of the warp's lanes, in every lane.
+__device__ __forceinline__ float warp_max_abs(float v) {
+    float r;
+    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // Pair sparse MMA that keeps its A operand in the tensor core's collector
 // buffer: kUse = 0 reads A from shared memory and keeps it (fill), kUse = 1
 // takes A from the collector and releases it (lastuse).  Two MMAs that share

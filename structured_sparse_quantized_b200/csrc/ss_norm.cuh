@@ -37,22 +37,28 @@ __device__ __forceinline__ void norm_weight16(const void* w, int wf32, int k0, i
         gload16<__nv_bfloat16>(static_cast<const __nv_bfloat16*>(w), k0, K, true, f);
 }
 
-// Scale factors of a row with the largest |z| = a: z -> RN(Q z / a).
+// Scale factors of a row with the largest |z| = a: z -> Q z / a, with Q / a
+// held as hi + lo to 2^-48, so that the sum of the two products is the
+// quotient rounded once (but for values within 2^-24 of halfway between two
+// fp32 numbers, which no code border is).
 template <int kQ>
 struct NormQuant {
-    float a, inv;
+    float a, hi, lo;
     __device__ __forceinline__ NormQuant(float amax) {
+        const float Q = q_max<kQ == kQInt8>();
+        const float inv = amax < kNormTiny ? 0.0f : __frcp_rn(amax);
         a = amax;
-        inv = amax < kNormTiny ? 0.0f : __frcp_rn(amax);
+        hi = Q * inv;
+        lo = fmaf(-hi, amax, Q) * inv;
     }
-    __device__ __forceinline__ float scaled(float z) const {
-        const float zq = z * q_max<kQ == kQInt8>();
-        const float p = zq * inv;
-        return fmaf(fmaf(-p, a, zq), inv, p);
+    __device__ __forceinline__ float scaled(float z) const { return fmaf(z, hi, z * lo); }
+    __device__ __forceinline__ void scaled2(float z0, float z1, float& p0, float& p1) const {
+        mul_rn_f32x2(z0, z1, lo, lo, p0, p1);
+        fma_rn_f32x2(z0, z1, hi, hi, p0, p1, p0, p1);
     }
-    // s_x of the row
+    // s_x of the row with factor r
     __device__ __forceinline__ float scale(float r) const {
-        return inv == 0.0f ? 0.0f : __fdiv_rn(a * r, q_max<kQ == kQInt8>());
+        return hi == 0.0f ? 0.0f : __fdiv_rn(a * r, q_max<kQ == kQInt8>());
     }
 };
 
@@ -70,90 +76,84 @@ __device__ __forceinline__ uint32_t norm_codes4(float p0, float p1, float p2, fl
     }
 }
 
-// Rows of up to 512 kChunks kWpr elements, read once: kWpr warps hold a row's
-// z in fp32 registers, 16 kChunks per lane; 8 / kWpr rows per CTA.  One
-// exchange gives the row's sum of squares and largest |z|.  Bound by HBM; with
-// z in registers each weight is read once per row, from L1.
-// q_stride: bytes of one row of codes in shared memory (4:6 and 8:10 only,
-// whose windows take codes of neighbouring lanes).
-template <typename T, int kQ, int kChunks, int kWpr>
-__global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
-    const T* __restrict__ X, const void* __restrict__ w, int wf32, float eps, int64_t M, int K,
-    int Nh, int K_lift, int K_lp, int q_stride, uint8_t* __restrict__ Xq,
-    float* __restrict__ s_x) {
-    extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int kRowsPerCta = kWarpRowThreads / (32 * kWpr);
-    constexpr int kRowThreads = 32 * kWpr;
-    constexpr bool kBf16 = kQ == kQBf16;
-    constexpr int kWords = kBf16 ? 8 : 4;  // 32-bit words of a chunk's codes
-    __shared__ float2 part[kRowsPerCta][kWpr];
-    pdl_trigger();
-    pdl_wait();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int slot = warp / kWpr, sub = warp % kWpr;
-    const int rt = sub * 32 + lane;
-    const int64_t m = static_cast<int64_t>(blockIdx.x) * kRowsPerCta + slot;
-    if (m >= M) return;  // a row's warps leave (or stay) together
-    const T* x = X + m * K;
-    const bool vec = K * static_cast<int>(sizeof(T)) % 16 == 0;
-    const int n16 = (K + 15) / 16;
-    const int c0 = sub * 32 * kChunks + lane;  // chunks c0 + 32 i, i < kChunks
-    float z[kChunks][16];
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) gload16<T>(x, (c0 + 32 * i) * 16, K, vec, z[i]);
-    float ss = 0.0f, a = 0.0f;
+// What a set of kWpr warps knows of the rows it works on.
+struct NormShape {
+    int K, Nh, K_lift, K_lp, n16;  // n16: 16-element chunks of a row, the last perhaps partial
+};
+
+// z = x w of this thread's chunks (in place of x), the row's sum of squares
+// and largest |z| over the warp.
+template <int kChunks, typename Weight>
+__device__ __forceinline__ float2 norm_products(float (&z)[kChunks][16], Weight weight) {
+    float s0 = 0.0f, s1 = 0.0f, a = 0.0f;
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         float f[16];
-        norm_weight16(w, wf32, (c0 + 32 * i) * 16, K, f);
+        weight(i, f);
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            ss = fmaf(z[i][j], z[i][j], ss);
-            z[i][j] *= f[j];
-            a = fmaxf(a, fabsf(z[i][j]));
+        for (int j = 0; j < 16; j += 2) {
+            float &z0 = z[i][j], &z1 = z[i][j + 1];
+            fma_rn_f32x2(z0, z1, z0, z1, s0, s1, s0, s1);
+            mul_rn_f32x2(z0, z1, f[j], f[j + 1], z0, z1);
+            a = max_abs3(a, z0, z1);
         }
     }
+    float s = s0 + s1;
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-    }
-    if constexpr (kWpr > 1) {
-        if (lane == 0) part[slot][sub] = make_float2(ss, a);
-        named_bar_sync(1 + slot, kRowThreads);
-        ss = a = 0.0f;
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return make_float2(s, warp_max_abs(a));
+}
+
+// The set's warps' parts together.
+template <int kWpr>
+__device__ __forceinline__ float2 norm_combine(const float2 (&part)[kWpr]) {
+    float2 v = part[0];
 #pragma unroll
-        for (int v = 0; v < kWpr; ++v) {
-            ss += part[slot][v].x;
-            a = fmaxf(a, part[slot][v].y);
-        }
+    for (int i = 1; i < kWpr; ++i) {
+        v.x += part[i].x;
+        v.y = fmaxf(v.y, part[i].y);
     }
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
-    const NormQuant<kQ> nq(a);
-    if constexpr (!kBf16) {
-        if (rt == 0) s_x[m] = nq.scale(r);
-    }
-    const int64_t row_bytes = static_cast<int64_t>(K_lp) * (kBf16 ? 2 : 1);
-    uint8_t* out = Xq + m * row_bytes;
-    uint4* qrow = reinterpret_cast<uint4*>(smem_raw + slot * q_stride);
+    return v;
+}
+
+// Writes one row's codes and scale from z; c0: this thread's first chunk (then
+// every 32nd), rt: its index in the set.  The windows of 4:6 and 8:10 take
+// codes of neighbouring threads, through the set's row of codes qrow.
+template <int kQ, int kChunks, int kWpr>
+__device__ __forceinline__ void norm_write_row(const float (&z)[kChunks][16], float2 sums,
+                                               float eps, const NormShape& s, int c0, int rt,
+                                               int bar, uint4* qrow, uint8_t* out, float* s_x) {
+    constexpr bool kBf16 = kQ == kQBf16;
+    constexpr int kWords = kBf16 ? 8 : 4;  // 32-bit words of a chunk's codes
+    constexpr int eb = kBf16 ? 2 : 1;
+    constexpr int kSetThreads = 32 * kWpr;
+    const int Nh = s.Nh, row_bytes = s.K_lp * eb;
+    const NormQuant<kQ> nq(sums.y);
+    float rn = 0.0f;
+    if (kBf16 || rt == 0) rn = 1.0f / sqrtf(sums.x / static_cast<float>(s.K) + eps);
+    if (!kBf16 && rt == 0) *s_x = nq.scale(rn);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
         const int c = c0 + 32 * i;
-        if (c >= n16) break;
+        if (c >= s.n16) break;
         uint32_t u[kWords];
         if constexpr (kBf16) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const __nv_bfloat162 h = __floats2bfloat162_rn(z[i][2 * j] * r, z[i][2 * j + 1] * r);
+                const __nv_bfloat162 h =
+                    __floats2bfloat162_rn(z[i][2 * j] * rn, z[i][2 * j + 1] * rn);
                 u[j] = *reinterpret_cast<const uint32_t*>(&h);
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                u[j] = norm_codes4<kQ>(nq.scaled(z[i][4 * j]), nq.scaled(z[i][4 * j + 1]),
-                                       nq.scaled(z[i][4 * j + 2]), nq.scaled(z[i][4 * j + 3]));
+            for (int j = 0; j < 4; ++j) {
+                float p[4];
+                nq.scaled2(z[i][4 * j], z[i][4 * j + 1], p[0], p[1]);
+                nq.scaled2(z[i][4 * j + 2], z[i][4 * j + 3], p[2], p[3]);
+                u[j] = norm_codes4<kQ>(p[0], p[1], p[2], p[3]);
+            }
         }
-        if (Nh <= 2 || Nh == 3 || Nh == 5) {  // in order: to the output, or to the code row
+        if (Nh <= 2 || Nh == 3 || Nh == 5) {  // in order: to the output, or the code row
             uint4* o = Nh <= 2 ? reinterpret_cast<uint4*>(out) : qrow;
 #pragma unroll
             for (int j = 0; j < kWords / 4; ++j) {
@@ -181,45 +181,189 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
                 if ((3 * c + j) * 8 < row_bytes) __stcs(o + j, v[j]);
         }
     }
-    const int eb = kBf16 ? 2 : 1;
     if (Nh <= 2 || Nh == 4) {  // zeros past the last chunk's windows
-        const int from = Nh <= 2 ? n16 * 16 * eb : n16 * 24 * eb;
-        for (int o = from / 8 + rt; o < row_bytes / 8; o += kRowThreads)
+        const int from = Nh <= 2 ? s.n16 * 16 * eb : s.n16 * 24 * eb;
+        for (int o = from / 8 + rt; o < row_bytes / 8; o += kSetThreads)
             __stcs(reinterpret_cast<uint2*>(out) + o, make_uint2(0, 0));
         return;
     }
-    // 4:6, 8:10: zero codes from the last chunk to one chunk past the last group
-    // (the reads below run at most one chunk past it), then the windows
-    const int q_chunks = ((K_lift / (4 * (Nh - 1))) * 2 * Nh * eb + 15) / 16;
-    for (int c = n16 * eb + rt; c <= q_chunks; c += kRowThreads) qrow[c] = make_uint4(0, 0, 0, 0);
-    if constexpr (kWpr > 1) named_bar_sync(1 + slot, kRowThreads);
+    // zero codes from the last chunk to one chunk past the last group: the
+    // reads below run at most that far
+    const int q_chunks = ((s.K_lift / (4 * (Nh - 1))) * 2 * Nh * eb + 15) / 16;
+    for (int c = s.n16 * eb + rt; c <= q_chunks; c += kSetThreads) qrow[c] = make_uint4(0, 0, 0, 0);
+    if constexpr (kWpr > 1) named_bar_sync(bar, kSetThreads);
     else __syncwarp();
-    // units: the 2-element words of the code row (uint16 of 8-bit codes, uint32
-    // of bf16); window i of group g is words Nh g + i, Nh g + i + 1
-    const int n_win = K_lift / 4, per = Nh - 1;
-    constexpr int kWin = kBf16 ? 2 : 4;  // windows per 16-byte store
-    for (int c = rt; c < row_bytes / 16; c += kRowThreads) {
-        int win = c * kWin, g = win / per, j = win - g * per;
-        uint32_t o[4];
-#pragma unroll
-        for (int i = 0; i < kWin; ++i) {
-            const int at = Nh * g + j;
-            const bool in = win + i < n_win;
+    // 16 output bytes of 8-bit codes are two 6-code groups or one 10-code
+    // group, of bf16 half of that
+    const int n_words = (s.K_lift * eb + 15) / 16;  // with windows (the rest are zero)
+    const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow);
+    for (int c = rt; c < row_bytes / 16; c += kSetThreads) {
+        uint4 o = make_uint4(0, 0, 0, 0);
+        if (c < n_words) {
             if constexpr (kBf16) {
-                const uint32_t* q32 = reinterpret_cast<const uint32_t*>(qrow);
-                o[2 * i] = in ? q32[at] : 0u;
-                o[2 * i + 1] = in ? q32[at + 1] : 0u;
+                // words of two codes; windows 2 c, 2 c + 1 of the row
+                const int at = Nh == 3 ? 3 * c : 5 * (c >> 1) + 2 * (c & 1);
+                o = make_uint4(q32[at], q32[at + 1], q32[at + 1], q32[at + 2]);
+            } else if (Nh == 3) {
+                // groups 2c, 2c + 1: code bytes 12c .. 12c + 11; windows at 0, 2, 6, 8
+                const uint32_t u0 = q32[3 * c], u1 = q32[3 * c + 1], u2 = q32[3 * c + 2];
+                o = make_uint4(u0, __byte_perm(u0, u1, 0x5432), __byte_perm(u1, u2, 0x5432), u2);
             } else {
-                const uint16_t* q16 = reinterpret_cast<const uint16_t*>(qrow);
-                o[i] = in ? q16[at] | (static_cast<uint32_t>(q16[at + 1]) << 16) : 0u;
-            }
-            if (++j == per) {
-                j = 0;
-                ++g;
+                // group c: code bytes 10c .. 10c + 9; windows at 0, 2, 4, 6
+                const int at = (10 * c) >> 2;
+                const uint32_t u0 = q32[at], u1 = q32[at + 1], u2 = q32[at + 2];
+                if ((c & 1) == 0)
+                    o = make_uint4(u0, __byte_perm(u0, u1, 0x5432), u1,
+                                   __byte_perm(u1, u2, 0x5432));
+                else
+                    o = make_uint4(__byte_perm(u0, u1, 0x5432), u1, __byte_perm(u1, u2, 0x5432),
+                                   u2);
             }
         }
-        __stcs(reinterpret_cast<uint4*>(out) + c, make_uint4(o[0], o[1], o[2], o[3]));
+        __stcs(reinterpret_cast<uint4*>(out) + c, o);
     }
+}
+
+// Rows of up to 512 kChunks kWpr elements, read once: kWpr warps hold a row's
+// z in fp32 registers, 16 kChunks per lane; 8 / kWpr rows per CTA.  For few
+// rows, and for rows that are not whole 16-byte words.
+template <typename T, int kQ, int kChunks, int kWpr>
+__global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
+    const T* __restrict__ X, const void* __restrict__ w, int wf32, float eps, int64_t M,
+    const NormShape s, int q_stride, uint8_t* __restrict__ Xq, float* __restrict__ s_x) {
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    constexpr int kSets = kWarpRowThreads / (32 * kWpr);
+    __shared__ float2 part[kSets][kWpr];
+    pdl_trigger();
+    pdl_wait();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int set = warp / kWpr, sub = warp % kWpr;
+    const int64_t m = static_cast<int64_t>(blockIdx.x) * kSets + set;
+    if (m >= M) return;  // a set's warps leave (or stay) together
+    const bool vec = s.K * static_cast<int>(sizeof(T)) % 16 == 0;
+    const int c0 = sub * 32 * kChunks + lane;  // chunks c0 + 32 i, i < kChunks
+    float z[kChunks][16];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i)
+        gload16<T>(X + m * s.K, (c0 + 32 * i) * 16, s.K, vec, z[i]);
+    float2 sums = norm_products<kChunks>(z, [&](int i, float (&f)[16]) {
+        norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f);
+    });
+    if constexpr (kWpr > 1) {
+        if (lane == 0) part[set][sub] = sums;
+        named_bar_sync(1 + set, 32 * kWpr);
+        sums = norm_combine<kWpr>(part[set]);
+    }
+    norm_write_row<kQ, kChunks, kWpr>(
+        z, sums, eps, s, c0, sub * 32 + lane, 1 + set,
+        reinterpret_cast<uint4*>(smem_raw + set * q_stride),
+        Xq + m * static_cast<int64_t>(s.K_lp) * (kQ == kQBf16 ? 2 : 1), s_x + m);
+}
+
+// Many rows of whole 16-byte words: CTAs stay, each set of kWpr warps keeps
+// the weights of its chunks in registers and kNormSlots rows in flight from
+// HBM into shared memory (1-D bulk copies), so that the copies of the next
+// rows go on while a row is reduced, quantised and stored.  Bound by HBM.
+// Without the copies in flight (rows straight to registers, 2 to 8 warps per
+// row) 16384 rows of 4096 took 50-89 us: the loads pause in every row's
+// reduction, and a weight read per row costs as much L1 time as the row.
+constexpr int kNormSlots = 4;
+
+template <typename T, int kQ, int kChunks, int kWpr>
+__global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel(
+    const T* __restrict__ X, const void* __restrict__ w, int wf32, float eps, int64_t M,
+    const NormShape s, int slot_stride, int q_stride, uint8_t* __restrict__ Xq,
+    float* __restrict__ s_x) {
+    extern __shared__ __align__(128) uint8_t smem_raw[];
+    constexpr int kSets = kWarpRowThreads / (32 * kWpr);
+    __shared__ uint64_t full[kSets][kNormSlots];
+    __shared__ float2 part[2][kSets][kWpr];
+    __shared__ int abort_flag_storage;
+    volatile int* abort_flag = &abort_flag_storage;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int set = warp / kWpr, sub = warp % kWpr;
+    const int rt = sub * 32 + lane;
+    const int c0 = sub * 32 * kChunks + lane;
+    if (threadIdx.x == 0) *abort_flag = 0;
+    if (rt == 0) {
+        for (int b = 0; b < kNormSlots; ++b) mbar_init(&full[set][b], 1);
+        fence_barrier_init();
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();
+    uint8_t* slots = smem_raw + set * (kNormSlots * slot_stride);
+    uint4* qrow = reinterpret_cast<uint4*>(smem_raw + kSets * kNormSlots * slot_stride +
+                                           set * q_stride);
+    const uint32_t bytes = static_cast<uint32_t>(s.K) * static_cast<uint32_t>(sizeof(T));
+    const int64_t step = static_cast<int64_t>(gridDim.x) * kSets;
+    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSets + set;
+    uint32_t issued = 0, taken = 0;  // rows copied and awaited (thread 0 of the set)
+    auto issue = [&](int64_t m) {
+        if (m >= M) return;
+        const uint32_t b = issued % kNormSlots;
+        mbar_arrive_expect_tx(&full[set][b], bytes);
+        bulk_load_1d(slots + b * slot_stride, X + m * s.K, bytes, &full[set][b]);
+        ++issued;
+    };
+    if (rt == 0)
+        for (int b = 0; b < kNormSlots; ++b) issue(m0 + b * step);
+    float f[kChunks][16];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
+    uint32_t it = 0;
+    for (int64_t m = m0; m < M; m += step, ++it) {
+        const uint32_t b = it % kNormSlots;
+        const bool got = mbar_wait(&full[set][b], (it / kNormSlots) & 1, abort_flag);
+        const T* x = reinterpret_cast<const T*>(slots + b * slot_stride);
+        float z[kChunks][16];
+#pragma unroll
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = c0 + 32 * i;
+            const uint4* v = reinterpret_cast<const uint4*>(x + c * 16);
+            constexpr int kVec = 16 / static_cast<int>(sizeof(T));
+#pragma unroll
+            for (int j = 0; j < 16 / kVec; ++j) {  // K is whole 16-byte words
+                const uint4 u = c * 16 + (j + 1) * kVec <= s.K ? v[j] : make_uint4(0, 0, 0, 0);
+                const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (sizeof(T) == 2) {
+                        z[i][8 * j + 2 * k] = __uint_as_float(uw[k] << 16);
+                        z[i][8 * j + 2 * k + 1] = __uint_as_float(uw[k] & 0xFFFF0000u);
+                    } else {
+                        z[i][4 * j + k] = __uint_as_float(uw[k]);
+                    }
+                }
+            }
+        }
+        float2 sums = norm_products<kChunks>(z, [&](int i, float (&g)[16]) {
+#pragma unroll
+            for (int j = 0; j < 16; ++j) g[j] = f[i][j];
+        });
+        bool all = got;
+        if constexpr (kWpr > 1) {
+            if (lane == 0) part[it & 1][set][sub] = sums;
+            // also: every warp of the set has read the slot, and is done with
+            // the code row and the parts of two rows ago
+            all = named_bar_and(1 + set, 32 * kWpr, got);
+            sums = norm_combine<kWpr>(part[it & 1][set]);
+        } else {
+            all = __all_sync(0xffffffffu, got);
+        }
+        if (!all) break;
+        if (rt == 0) {
+            taken = it + 1;
+            fence_async_shared();
+            issue(m + kNormSlots * step);
+        }
+        norm_write_row<kQ, kChunks, kWpr>(
+            z, sums, eps, s, c0, rt, 1 + set, qrow,
+            Xq + m * static_cast<int64_t>(s.K_lp) * (kQ == kQBf16 ? 2 : 1), s_x + m);
+    }
+    if (rt == 0)  // after a wait that ran out: copies in flight land before exit
+        for (; taken < issued; ++taken)
+            mbar_drain(&full[set][taken % kNormSlots], (taken / kNormSlots) & 1);
 }
 
 // One block per token row, any K.  The output is walked in lifted order, each

@@ -66,6 +66,16 @@ def test_patterns_tiers_sizes(pattern, tier, dtype, M, K):
     check(X, w.to(BF if K % 3 else F32), 1e-5, pattern, tier)
 
 
+@pytest.mark.parametrize("pattern", ["dense", "4:6", "6:8", "8:10"])
+@pytest.mark.parametrize("tier", ["int8", "fp8", "bf16"])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("M,K", [(1500, 4096), (2500, 264), (4003, 1000), (1300, 2040), (1200, 5000),
+                                 (1184, 8), (1200, 4097)])
+def test_many_rows(pattern, tier, dtype, M, K):
+    X, w = rows(M, K, dtype)
+    check(X, w.to(BF if M % 2 else F32), 1e-5, pattern, tier)
+
+
 @pytest.mark.parametrize("tier", ["int8", "fp8", "bf16"])
 def test_zero_rows_tiny_rows_and_eps(tier):
     X, w = rows(8, 256, F32)
