@@ -33,8 +33,8 @@ Convenience wrappers that allocate their outputs with torch:
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
+import functools
 import os
 
 import torch
@@ -519,37 +519,85 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
 # call, and run on the device of their tensors, on its current stream, whatever
 # device is current.
 
-def _here(t: torch.Tensor):
-    """Context that makes t's device current (none needed when it already is)."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+class _On:
+    """Makes device `index` current for a call, and `old` again after it."""
+
+    def __init__(self, index: int, old: int):
+        self.index, self.old = index, old
+
+    def __enter__(self):
+        if self.index != self.old:
+            torch.cuda.set_device(self.index)
+
+    def __exit__(self, *_):
+        if self.index != self.old:
+            torch.cuda.set_device(self.old)
 
 
-def _raw_stream(stream, t: torch.Tensor) -> int:
+def _on(index: int) -> _On:
+    return _On(index, torch.cuda.current_device())
+
+
+def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(t.device).cuda_stream
+        return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
-def _arg(t, name: str, shape=None, dtypes=None, like=None, contiguous=True) -> int:
-    """Data pointer of a checked CUDA tensor (None stays None)."""
-    if t is None:
-        return None
+def _index(t, name: str) -> int:
+    """Index of the CUDA device that t is on."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if contiguous and not t.is_contiguous():
+    return t.get_device()
+
+
+def _arg(t, name: str, shape, dtypes, index: int):
+    """Data pointer of a contiguous CUDA tensor on device `index` with that
+    shape (None: any) and one of the types; None stays None."""
+    if t is None:
+        return None
+    if _index(t, name) == index and t.is_contiguous() and (shape is None or t.shape == shape) \
+            and t.dtype in dtypes:
+        return t.data_ptr()
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, not cuda:{index}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError(f"{name} dtype {t.dtype} not supported")
-    if like is not None and t.device != like.device:
-        raise ValueError(f"{name} is on {t.device}, not {like.device}")
-    return t.data_ptr()
+    raise ValueError(f"{name} dtype {t.dtype} not supported")
+
+
+def _need(t, name: str, shape, dtypes, index: int):
+    if t is None:
+        raise ValueError(f"{name} is required")
+    return _arg(t, name, shape, dtypes, index)
+
+
+@functools.lru_cache(maxsize=None)
+def _pattern_of(keep: int, group: int) -> ss_pattern:
+    return ss_pattern(keep, group)
+
+
+@functools.lru_cache(maxsize=1024)
+def _pattern_named(s: str) -> ss_pattern:
+    return _pattern(s)
+
+
+@functools.lru_cache(maxsize=4096)
+def _k_lp(keep: int, group: int, K: int) -> int:
+    return ss_slide_shape(_pattern_of(keep, group), K)[2]
+
+
+def _pattern_k_lp(pattern, K: int):
+    p = _pattern_named(pattern) if isinstance(pattern, str) else _pattern(pattern)
+    return p, _k_lp(p.keep, p.group, K)
 
 
 _FLOATS = (torch.bfloat16, torch.float32)
+_F32 = (torch.float32,)
+_BYTES = (torch.uint8,)
+_IN = {torch.float32: SS_IN_F32, torch.bfloat16: SS_IN_BF16}
 
 
 class Epilogue:
@@ -575,104 +623,95 @@ class Epilogue:
         return torch.empty((M, N // 2 if self.gated else N), dtype=out_dtype, device=device)
 
     def _args(self, M, N, Y):
-        """(ss_epilogue, Y's pointer), checked against the product's shape."""
-        y = _arg(Y, "Y", (M, N // 2 if self.gated else N), _FLOATS)
-        if y is None:
-            raise ValueError("Y must be a CUDA tensor")
-        e = ss_epilogue(_arg(self.bias, "bias", (N,), _FLOATS, Y),
-                        _arg(self.residual, "residual", (M, N), _FLOATS, Y), SS_IN_BF16,
-                        SS_IN_BF16, ACTS[self.act], int(self.gated))
-        if self.bias is not None:
-            e.bias_dtype = _in_dtype(self.bias)
-        if self.residual is not None:
-            e.residual_dtype = _in_dtype(self.residual)
-        return e, y
+        """(ss_epilogue, Y's pointer, Y's device), checked against the product's shape."""
+        d = _index(Y, "Y")
+        y = _arg(Y, "Y", (M, N // 2 if self.gated else N), _FLOATS, d)
+        b, r = self.bias, self.residual
+        e = ss_epilogue(_arg(b, "bias", (N,), _FLOATS, d), _arg(r, "residual", (M, N), _FLOATS, d),
+                        SS_IN_BF16 if b is None else _IN[b.dtype],
+                        SS_IN_BF16 if r is None else _IN[r.dtype], ACTS[self.act], self.gated)
+        return e, y, d
 
 
-def _stored(q) -> tuple:
-    """(element types of stored values, scaled?) of an operand of type q."""
-    if q == SS_BF16:
-        return (torch.bfloat16,), False
-    return (torch.uint8, torch.int8, torch.float8_e4m3fn), True
+_STORED_8BIT = (torch.uint8, torch.int8, torch.float8_e4m3fn)
+_STORED_BF16 = (torch.bfloat16,)
 
 
-def _scale_arg(s, name, n, scaled, like):
-    if not scaled:
-        return None
-    if s is None:
-        raise ValueError(f"{name} is required")
-    return _arg(s, name, (n,), (torch.float32,), like)
+def _scale_arg(s, name, n, q, d):
+    return None if q == SS_BF16 else _need(s, name, (n,), _F32, d)
+
+
+def _bytes_arg(t, name, n, d):
+    """Pointer of a byte tensor of any shape with n elements."""
+    p = _need(t, name, None, _BYTES, d)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} bytes, got {t.numel()}")
+    return p
 
 
 def ss_sparse_gemm_fused(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: int, K_lp: int, q,
                          epilogue: Epilogue, Y, stream=None) -> None:
     q = _qdtype(q)
-    e, y = epilogue._args(M, N, Y)
+    e, y, d = epilogue._args(M, N, Y)
     rows_a, rows_b = (M, N) if sparse_operand else (N, M)
-    vals, scaled = _stored(q)
-    a = _arg(Av, "Av", (rows_a, K_lp // 2), vals, Y)
-    m = _arg(Am, "Am", None, (torch.uint8,), Y)
-    if Am is not None and Am.numel() != ss_meta_bytes(rows_a, K_lp):
-        raise ValueError(f"Am must have {ss_meta_bytes(rows_a, K_lp)} bytes, got {Am.numel()}")
-    b = _arg(B, "B", (rows_b, K_lp), vals, Y)
-    sa = _scale_arg(s_a, "s_a", rows_a, scaled, Y)
-    sb = _scale_arg(s_b, "s_b", rows_b, scaled, Y)
-    with _here(Y):
+    vals = _STORED_BF16 if q == SS_BF16 else _STORED_8BIT
+    a = _need(Av, "Av", (rows_a, K_lp // 2), vals, d)
+    m = _bytes_arg(Am, "Am", (rows_a + 127) // 128 * 16 * K_lp, d)
+    b = _need(B, "B", (rows_b, K_lp), vals, d)
+    sa, sb = _scale_arg(s_a, "s_a", rows_a, q, d), _scale_arg(s_b, "s_b", rows_b, q, d)
+    with _on(d):
         _check(lib().ss_sparse_gemm_fused(sparse_operand, a, m, sa, b, sb, M, N, K_lp, q,
                                           ctypes.byref(e), y, _out_dtype(Y),
-                                          _raw_stream(stream, Y)), "ss_sparse_gemm_fused")
+                                          _raw_stream(stream, d)), "ss_sparse_gemm_fused")
 
 
 def ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M: int, N: int, K_p: int, q, epilogue: Epilogue, Y,
                         stream=None) -> None:
     q = _qdtype(q)
-    e, y = epilogue._args(M, N, Y)
-    vals, scaled = _stored(q)
-    x = _arg(Xq, "Xq", (M, K_p), vals, Y)
-    w = _arg(Wq, "Wq", (N, K_p), vals, Y)
-    sx = _scale_arg(s_x, "s_x", M, scaled, Y)
-    sw = _scale_arg(s_w, "s_w", N, scaled, Y)
-    with _here(Y):
+    e, y, d = epilogue._args(M, N, Y)
+    vals = _STORED_BF16 if q == SS_BF16 else _STORED_8BIT
+    x, w = _need(Xq, "Xq", (M, K_p), vals, d), _need(Wq, "Wq", (N, K_p), vals, d)
+    sx, sw = _scale_arg(s_x, "s_x", M, q, d), _scale_arg(s_w, "s_w", N, q, d)
+    with _on(d):
         _check(lib().ss_dense_gemm_fused(x, sx, w, sw, M, N, K_p, q, ctypes.byref(e), y,
-                                         _out_dtype(Y), _raw_stream(stream, Y)),
+                                         _out_dtype(Y), _raw_stream(stream, d)),
                "ss_dense_gemm_fused")
 
 
-def _fp4_arg(t, name, rows, cols, like):
-    return _arg(t, name, (rows, cols), (torch.uint8,), like)
+def _fp4_scales(s, name, rows, K_lp, block, d):
+    return _bytes_arg(s, name, ss_fp4_scale_bytes(rows, K_lp, block), d)
 
 
-def _fp4_scales(s, name, rows, K_lp, block, like):
-    n = ss_fp4_scale_bytes(rows, K_lp, block)
-    if s is not None and s.numel() != n:
-        raise ValueError(f"{name} must have {n} bytes, got {s.numel()}")
-    return _arg(s, name, None, (torch.uint8,), like)
+def _global_scale(g, name, d):
+    p = _need(g, name, None, _F32, d)
+    if g.numel() < 1:
+        raise ValueError(f"{name} is empty")
+    return p
 
 
 def ss_sparse_gemm_nvfp4_fused(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M: int, N: int, K_lp: int,
                                epilogue: Epilogue, Y, stream=None) -> None:
-    e, y = epilogue._args(M, N, Y)
-    m = _arg(Wm, "Wm", None, (torch.uint8,), Y)
-    if Wm is not None and Wm.numel() != ss_meta_bytes(N, K_lp // 2):
-        raise ValueError(f"Wm must have {ss_meta_bytes(N, K_lp // 2)} bytes, got {Wm.numel()}")
-    args = (_fp4_arg(Wv, "Wv", N, K_lp // 4, Y), m, _fp4_scales(Ws, "Ws", N, K_lp, 32, Y),
-            _arg(g_w, "g_w", None, (torch.float32,), Y), _fp4_arg(Xv, "Xv", M, K_lp // 2, Y),
-            _fp4_scales(Xs, "Xs", M, K_lp, 32, Y), _arg(g_x, "g_x", None, (torch.float32,), Y))
-    with _here(Y):
+    e, y, d = epilogue._args(M, N, Y)
+    args = (_need(Wv, "Wv", (N, K_lp // 4), _BYTES, d),
+            _bytes_arg(Wm, "Wm", ss_meta_bytes(N, K_lp // 2), d),
+            _fp4_scales(Ws, "Ws", N, K_lp, 32, d), _global_scale(g_w, "g_w", d),
+            _need(Xv, "Xv", (M, K_lp // 2), _BYTES, d), _fp4_scales(Xs, "Xs", M, K_lp, 32, d),
+            _global_scale(g_x, "g_x", d))
+    with _on(d):
         _check(lib().ss_sparse_gemm_nvfp4_fused(*args, M, N, K_lp, ctypes.byref(e), y,
-                                                _out_dtype(Y), _raw_stream(stream, Y)),
+                                                _out_dtype(Y), _raw_stream(stream, d)),
                "ss_sparse_gemm_nvfp4_fused")
 
 
 def ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M: int, N: int, K_p: int,
                               epilogue: Epilogue, Y, stream=None) -> None:
-    e, y = epilogue._args(M, N, Y)
-    args = (_fp4_arg(Xv, "Xv", M, K_p // 2, Y), _fp4_scales(Xs, "Xs", M, K_p, 16, Y),
-            _arg(g_x, "g_x", None, (torch.float32,), Y), _fp4_arg(Wv, "Wv", N, K_p // 2, Y),
-            _fp4_scales(Ws, "Ws", N, K_p, 16, Y), _arg(g_w, "g_w", None, (torch.float32,), Y))
-    with _here(Y):
+    e, y, d = epilogue._args(M, N, Y)
+    args = (_need(Xv, "Xv", (M, K_p // 2), _BYTES, d), _fp4_scales(Xs, "Xs", M, K_p, 16, d),
+            _global_scale(g_x, "g_x", d), _need(Wv, "Wv", (N, K_p // 2), _BYTES, d),
+            _fp4_scales(Ws, "Ws", N, K_p, 16, d), _global_scale(g_w, "g_w", d))
+    with _on(d):
         _check(lib().ss_dense_gemm_nvfp4_fused(*args, M, N, K_p, ctypes.byref(e), y,
-                                               _out_dtype(Y), _raw_stream(stream, Y)),
+                                               _out_dtype(Y), _raw_stream(stream, d)),
                "ss_dense_gemm_nvfp4_fused")
 
 
@@ -691,34 +730,30 @@ def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
 
 def ss_norm_quant_lift_act(X, weight, eps: float, pattern, q, Xq_lift, s_x, stream=None) -> None:
     q = _qdtype(q)
-    x = _arg(X, "X", None, _FLOATS)
-    if X is None or X.dim() != 2:
+    d = _index(X, "X")
+    if X.dim() != 2:
         raise ValueError("X must be a [M, K] CUDA tensor")
     M, K = X.shape
-    _, _, K_lp = ss_slide_shape(pattern, K)
-    vals, scaled = _stored(q)
-    w = _arg(weight, "weight", (K,), _FLOATS, X)
-    if w is None:
-        raise ValueError("weight must be a CUDA tensor")
-    xq = _arg(Xq_lift, "Xq_lift", (M, K_lp), vals, X)
-    sx = _scale_arg(s_x, "s_x", M, scaled, X)
-    with _here(X):
-        _check(lib().ss_norm_quant_lift_act(x, _in_dtype(X), w, _in_dtype(weight), float(eps), M,
-                                            K, _pattern(pattern), q, xq, sx,
-                                            _raw_stream(stream, X)), "ss_norm_quant_lift_act")
+    p, K_lp = _pattern_k_lp(pattern, K)
+    x = _arg(X, "X", None, _FLOATS, d)
+    w = _need(weight, "weight", (K,), _FLOATS, d)
+    xq = _need(Xq_lift, "Xq_lift", (M, K_lp), _STORED_BF16 if q == SS_BF16 else _STORED_8BIT, d)
+    sx = _scale_arg(s_x, "s_x", M, q, d)
+    with _on(d):
+        _check(lib().ss_norm_quant_lift_act(x, _IN[X.dtype], w, _IN[weight.dtype], eps, M, K, p, q,
+                                            xq, sx, _raw_stream(stream, d)),
+               "ss_norm_quant_lift_act")
 
 
 def norm_quant_lift_act(X: torch.Tensor, weight: torch.Tensor, eps: float, pattern, q,
                         stream=None, out=None):
     """RMS norm of X's rows, quantised and lifted as quant_lift_act does;
     -> (Xq_lift [M, K_lp], s_x [M], or None for the bf16 tier)."""
-    p = _pattern(pattern)
     if out is None:
         M, K = X.shape
-        _, _, K_lp = ss_slide_shape(p, K)
-        out = (torch.empty((M, K_lp), dtype=_vals_dtype(q), device=X.device),
-               _scales(M, q, X.device))
-    ss_norm_quant_lift_act(X, weight, eps, p, q, out[0], out[1], stream)
+        out = (torch.empty((M, _pattern_k_lp(pattern, K)[1]), dtype=_vals_dtype(q),
+                           device=X.device), _scales(M, q, X.device))
+    ss_norm_quant_lift_act(X, weight, eps, pattern, q, out[0], out[1], stream)
     return out
 
 
@@ -748,39 +783,41 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "none", fa
     return torch.tensor(f, dtype=torch.float64, device=device), scale
 
 
-def _heads(x, y, name, T, D, like) -> ss_rope_heads:
-    p = _arg(x, name, None, (like.dtype,), like, contiguous=False)
-    o = _arg(y, f"{name} output", x.shape, (like.dtype,), like, contiguous=False)
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
-        raise ValueError(f"{name} must be [{T}, heads, {D}], got {tuple(x.shape)}")
-    for t, what in ((x, name), (y, f"{name} output")):
-        if D > 1 and t.stride(2) != 1:
-            raise ValueError(f"{what}: the elements of a head must be contiguous")
-    if any(n > 1 and s == 0 for n, s in zip(y.shape, y.stride())):
-        raise ValueError(f"{name} output: elements overlap")
-    return ss_rope_heads(p, o, x.shape[1], x.stride(0), x.stride(1), y.stride(0), y.stride(1))
+def _heads(x, y, name, T, D, dtype, d) -> ss_rope_heads:
+    for t, what in ((x, name), (y, f"{name}'s output")):
+        if _index(t, what) != d or t.dtype != dtype:
+            raise ValueError(f"{what} must be {dtype} on cuda:{d}, like q")
+    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or y.shape != x.shape:
+        raise ValueError(f"{name} and its output must be [{T}, heads, {D}], got {tuple(x.shape)} "
+                         f"and {tuple(y.shape)}")
+    (st, sh, se), (ot, oh, oe), H = x.stride(), y.stride(), x.shape[1]
+    if se != 1 or oe != 1:
+        raise ValueError(f"{name}: the elements of a head must be contiguous")
+    if (T > 1 and abs(ot) < 1) or (H > 1 and abs(oh) < 1):
+        raise ValueError(f"{name}'s output: its elements overlap")
+    return ss_rope_heads(x.data_ptr(), y.data_ptr(), H, st, sh, ot, oh)
 
 
 def ss_rope(q, k, positions, freqs, layout, scale: float, q_out, k_out, stream=None) -> None:
-    if q is None or q.dim() != 3:
-        raise ValueError("q must be a [T, heads, head_dim] CUDA tensor")
+    d = _index(q, "q")
+    if q.dim() != 3 or q.dtype not in _FLOATS:
+        raise ValueError("q must be a [T, heads, head_dim] float32 or bfloat16 tensor")
     if (k is None) != (k_out is None):
         raise ValueError("k and its output go together")
     layout = ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
     T, _, D = q.shape
-    hq = _heads(q, q_out, "q", T, D, q)
-    hk = None if k is None else _heads(k, k_out, "k", T, D, q)
-    if q.dtype not in _FLOATS:
-        raise ValueError(f"q dtype {q.dtype} not supported (float32 or bfloat16)")
-    pos = _arg(positions, "positions", (T,), (torch.int32, torch.int64), q)
-    f = _arg(freqs, "freqs", None, (torch.float64,), q)
-    if pos is None or f is None:
-        raise ValueError("positions and freqs must be CUDA tensors")
-    with _here(q):
-        _check(lib().ss_rope(ctypes.byref(hq), None if hk is None else ctypes.byref(hk),
-                             _in_dtype(q), pos, int(positions.dtype == torch.int64), f,
-                             float(scale), T, D, 2 * freqs.numel(), layout,
-                             _raw_stream(stream, q)), "ss_rope")
+    hq = _heads(q, q_out, "q", T, D, q.dtype, d)
+    hk = None if k is None else ctypes.byref(_heads(k, k_out, "k", T, D, q.dtype, d))
+    pos = _need(positions, "positions", (T,), _INTS, d)
+    f = _need(freqs, "freqs", None, _F64, d)
+    with _on(d):
+        _check(lib().ss_rope(ctypes.byref(hq), hk, _IN[q.dtype], pos,
+                             positions.dtype == torch.int64, f, scale, T, D, 2 * freqs.numel(),
+                             layout, _raw_stream(stream, d)), "ss_rope")
+
+
+_INTS = (torch.int32, torch.int64)
+_F64 = (torch.float64,)
 
 
 def rope(q: torch.Tensor, k, positions: torch.Tensor, freqs: torch.Tensor, layout="half",
