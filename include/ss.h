@@ -175,7 +175,8 @@ ss_status ss_dense_gemm(const void *Xq, const float *s_x, const void *Wq, const 
 
 /* What a fused GEMM does to an output before its one rounding to Y's type
  * (bias, activation and residual of a transformer's projections), all in
- * fp32 on v[m, n] = the plain call's fp32 value + bias[n]:
+ * fp32 on v[m, n] = fma((float)acc[m, n] * s_x[m], s_w[n], bias[n]), which
+ * without a bias is the plain call's fp32 value:
  *   plain:  Y[m, n]         = act(v[m, n]) + residual[m, n]     Y is [M, N]
  *   gated:  Y[m, 8 g + i]   = act(v[m, 16 g + i]) * v[m, 16 g + 8 + i],
  *           i = 0..7                                            Y is [M, N/2]

@@ -360,12 +360,12 @@ int kernel_q(ss_qdtype q) {
     return -1;
 }
 
-template <bool kInt8, bool kAIsW>
+template <bool kInt8, bool kAIsW, bool kEpi = false>
 ss_status launch_gemm_wide(int dev, const CUtensorMap& a, const CUtensorMap& b,
-                           const CUtensorMap& e, const CUtensorMap& y, const ss::GemmArgs& args,
-                           cudaStream_t stream) {
-    using C = ss::WideCfg;
-    auto kern = ss::gemm_sparse_wide_kernel<kInt8, kAIsW>;
+                           const CUtensorMap& e, const CUtensorMap& y, const CUtensorMap& r,
+                           const ss::GemmArgs& args, cudaStream_t stream) {
+    using C = ss::WideCfg<kEpi>;
+    auto kern = ss::gemm_sparse_wide_kernel<kInt8, kAIsW, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
     std::call_once(once[dev], [&] {
@@ -379,7 +379,7 @@ ss_status launch_gemm_wide(int dev, const CUtensorMap& a, const CUtensorMap& b,
     const int64_t units = g_num_sms[dev] / 2;
     const int grid = static_cast<int>((tiles < units ? tiles : units) * 2);
     return launch_ex(kern, dim3(grid), dim3(ss::kWideThreads), C::kSmemBytes, stream, 2, a, b, e,
-                     y, args);
+                     y, r, args);
 }
 
 // B-tile width of the wide sparse GEMM: the multiple of 32 (<= 224) whose
@@ -389,10 +389,10 @@ ss_status launch_gemm_wide(int dev, const CUtensorMap& a, const CUtensorMap& b,
 // tile), which is what bounds the mainloop.
 int choose_bn_wide(int64_t rowsA, int64_t rowsB, int units) {
     const int64_t nA = (rowsA + 2 * ss::kTileA - 1) / (2 * ss::kTileA);
-    int best = ss::WideCfg::kBnMax;
+    int best = ss::WideCfg<>::kBnMax;
     double best_cost = 0.0;
     std::vector<double> load(static_cast<size_t>(units));
-    for (int bn = ss::WideCfg::kBnMax; bn >= 64; bn -= 32) {
+    for (int bn = ss::WideCfg<>::kBnMax; bn >= 64; bn -= 32) {
         const int64_t nB = (rowsB + 2 * bn - 1) / (2 * bn);
         const int64_t tiles = nA * nB;
         std::fill(load.begin(), load.end(), 0.0);
@@ -403,7 +403,7 @@ int choose_bn_wide(int64_t rowsA, int64_t rowsB, int units) {
             load[static_cast<size_t>(u)] += 5120.0 + 32.0 * static_cast<double>(tok);
         }
         const double cost = *std::max_element(load.begin(), load.end());
-        if (bn == ss::WideCfg::kBnMax || cost < best_cost * 0.98) {
+        if (bn == ss::WideCfg<>::kBnMax || cost < best_cost * 0.98) {
             best = bn;
             best_cost = cost;
         }
@@ -431,7 +431,7 @@ int forced_sparse_kernel() {
 bool prefer_wide(int64_t rowsA, int64_t rowsB, int bn_narrow, int units) {
     const int64_t nA = (rowsA + 2 * ss::kTileA - 1) / (2 * ss::kTileA);
     const int64_t waves_n = (nA * ((rowsB + bn_narrow - 1) / bn_narrow) + units - 1) / units;
-    const int64_t tile_w = 2 * ss::WideCfg::kBnMax;
+    const int64_t tile_w = 2 * ss::WideCfg<>::kBnMax;
     const int64_t waves_w = (nA * ((rowsB + tile_w - 1) / tile_w) + units - 1) / units;
     return 1.8 * static_cast<double>(waves_w) < static_cast<double>(waves_n);
 }
@@ -614,10 +614,10 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
     // (8-bit operands only: the bf16 tier runs the one-B-tile kernel)
     // Large problems with bf16 Y may take two B tiles per output tile: fewer
     // bytes per MMA, but single-buffered accumulators.
-    if (scaled && !fused && pair == 2 && args.tma_store && forced != 1 &&
-        (forced == 2 || (rowsB > 2 * ss::WideCfg::kBnMax &&
+    if (scaled && pair == 2 && args.tma_store && forced != 1 &&
+        (forced == 2 || (rowsB > 2 * ss::WideCfg<>::kBnMax &&
                          prefer_wide(rowsA, rowsB, bn, g_num_sms[dev] / 2)))) {
-        using CW = ss::WideCfg;
+        using CW = ss::WideCfg<>;
         const int bnw = choose_bn_wide(rowsA, rowsB, g_num_sms[dev] / 2);
         CUtensorMap wa, wb;
         if (!make_map_2d(&wa, Av, rowsA, K_lp / 2, ss::kTileA, CW::kARowBytes,
@@ -629,11 +629,14 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
         wargs.a_groups = a_groups_for(rowsA * (K_lp / 2 + K_lp / 8), (rowsA + 255) / 256,
                                       g_num_sms[dev] / 2, 2 * static_cast<int64_t>(bnw) * K_lp);
         wargs.k_stages = static_cast<int>(K_lp / CW::kStageK);
+        if (fused)  // (TMA stores: channel rows)
+            return i8 ? launch_gemm_wide<true, true, true>(dev, wa, wb, te, ty, tr, wargs, st_)
+                      : launch_gemm_wide<false, true, true>(dev, wa, wb, te, ty, tr, wargs, st_);
         if (args.a_is_w)
-            return i8 ? launch_gemm_wide<true, true>(dev, wa, wb, te, ty, wargs, st_)
-                      : launch_gemm_wide<false, true>(dev, wa, wb, te, ty, wargs, st_);
-        return i8 ? launch_gemm_wide<true, false>(dev, wa, wb, te, ty, wargs, st_)
-                  : launch_gemm_wide<false, false>(dev, wa, wb, te, ty, wargs, st_);
+            return i8 ? launch_gemm_wide<true, true>(dev, wa, wb, te, ty, tr, wargs, st_)
+                      : launch_gemm_wide<false, true>(dev, wa, wb, te, ty, tr, wargs, st_);
+        return i8 ? launch_gemm_wide<true, false>(dev, wa, wb, te, ty, tr, wargs, st_)
+                  : launch_gemm_wide<false, false>(dev, wa, wb, te, ty, tr, wargs, st_);
     }
 #endif
     return dispatch_gemm_any<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, tr, args, st_);

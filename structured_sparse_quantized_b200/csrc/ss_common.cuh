@@ -722,6 +722,34 @@ __device__ __forceinline__ void fma_rn_f32x2(float a0, float a1, float b0, float
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
 }
 
+__device__ __forceinline__ void add_rn_f32x2(float a0, float a1, float b0, float b1, float& r0,
+                                             float& r1) {
+    uint64_t a, b, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(a) : "f"(a0), "f"(a1));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(b) : "f"(b0), "f"(b1));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r0), "=f"(r1) : "l"(r));
+}
+
+// 2^x and 1 / x, each to 2 units of 2^-23 or better; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float rcp_fast(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// max(v, 0), NaN stays.
+__device__ __forceinline__ float relu_nan(float v) {
+    float r;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(r) : "f"(v));
+    return r;
+}
+
 // max(a, |b|, |c|) for a >= 0; NaN operands are passed over.
 __device__ __forceinline__ float max_abs3(float a, float b, float c) {
     float r;

@@ -1,11 +1,12 @@
 // ss_epilogue.cuh -- what the fused GEMM entry points do to an accumulator
 // between the dequantisation and the one rounding to Y's type:
 //
-//   v[m, n] = ((float)acc[m, n] * s_x[m]) * s_w[n] + bias[n]
+//   v[m, n] = fma((float)acc[m, n] * s_x[m], s_w[n], bias[n])
 //   plain:  Y[m, n]         = act(v[m, n]) + residual[m, n]
 //   gated:  Y[m, 8 g + i]   = act(v[m, 16 g + i]) * v[m, 16 g + 8 + i],  i < 8
 //
-// all in fp32.  A gated weight holds its rows in groups of 16, eight gates
+// all in fp32; without a bias v is the plain product's fp32 value.  A gated
+// weight holds its rows in groups of 16, eight gates
 // and then their eight partners: the two factors of an output then sit 8 rows
 // apart inside one 16-row group, which no kernel shape splits (tiles, K-split
 // reduction slices and tensor-memory lane quarters are multiples of 16), and
@@ -31,36 +32,90 @@ struct EpiArgs {
     int gated;
 };
 
+// Activations, two values at a time (packed fp32 arithmetic).
+//
 // silu(v) = v / (1 + e^-v).  The tanh form of GELU is v / (1 + e^-2u) with
 // u = sqrt(2/pi) (v + 0.044715 v^3), because (1 + tanh u) / 2 = 1 / (1 + e^-2u):
-// unlike 1 + tanh u it does not cancel for negative v.  For the same reason
-// the exact form is v erfc(-v / sqrt 2) / 2.  The fast exponential and divide
-// are within a few units of 2^-23, far below the rounding to bf16 and within
-// what fp32 products of this length carry; e^-v = inf gives -0.
+// unlike 1 + tanh u it does not cancel for negative v.
+//
+// The exact GELU is v Phi(v) = max(v, 0) - |v| Phi(-|v|), and Phi(-u) =
+// e^(-u^2 / 2) G(u) with G(u) = erfcx(u / sqrt 2) / 2 smooth and slowly falling:
+// G = t Q(t) with t = 1 / (1 + 0.34 u) and a polynomial Q of degree 8 fitted to
+// the least relative error over u in [0, 16] (4.7e-8; 2.7 units of 2^-23 with
+// the fp32 evaluation).  Unlike v (1 + erf) / 2 it keeps its digits for
+// negative v, at two special-function operations a value; CUDA's erfcf in this
+// place took the epilogue of a 256 x 224 tile past its MMAs (8192 x 4096 x
+// 4096 2:4 INT8: 149 us against 63 for the plain product).
+//
+// Each result is within a few units of 2^-23 (plus those of the exponent, which
+// grow with it), far below the rounding to bf16.  e^-v = inf gives -0.
 template <int kAct>
-__device__ __forceinline__ float activate(float v) {
+__device__ __forceinline__ void activate2(float& v0, float& v1) {
     if constexpr (kAct == kActRelu) {
-        return v < 0.0f ? 0.0f : v;  // NaN stays
-    } else if constexpr (kAct == kActSilu) {
-        return __fdividef(v, 1.0f + __expf(-v));
-    } else if constexpr (kAct == kActGelu) {
-        const float u2 = v * fmaf(0.0713548162726f, v * v, 1.5957691216057f);  // 2 u
-        return __fdividef(v, 1.0f + __expf(-u2));
+        v0 = relu_nan(v0);
+        v1 = relu_nan(v1);
+    } else if constexpr (kAct == kActSilu || kAct == kActGelu) {
+        float x0, x1;  // -(exponent of e) log2(e)
+        if constexpr (kAct == kActSilu) {
+            mul_rn_f32x2(v0, v1, -1.4426950409f, -1.4426950409f, x0, x1);
+        } else {
+            constexpr float c1 = -2.3022081986f;  // -2 sqrt(2 / pi) log2 e
+            constexpr float c3 = -0.10294323960f;  // 0.044715 c1
+            mul_rn_f32x2(v0, v1, v0, v1, x0, x1);
+            fma_rn_f32x2(x0, x1, c3, c3, c1, c1, x0, x1);
+            mul_rn_f32x2(x0, x1, v0, v1, x0, x1);
+        }
+        x0 = ex2_fast(x0);
+        x1 = ex2_fast(x1);
+        add_rn_f32x2(x0, x1, 1.0f, 1.0f, x0, x1);
+        mul_rn_f32x2(v0, v1, rcp_fast(x0), rcp_fast(x1), v0, v1);
     } else if constexpr (kAct == kActGeluErf) {
-        return 0.5f * v * erfcf(v * -0.70710678118655f);
-    } else {
-        return v;
+        // |v| is cut at 16, where Phi(-u) is 0 in fp32, so that infinities pass
+        const float u0 = fminf(fabsf(v0), 16.0f), u1 = fminf(fabsf(v1), 16.0f);
+        float t0, t1, e0, e1, q0, q1;
+        fma_rn_f32x2(u0, u1, 0.34f, 0.34f, 1.0f, 1.0f, t0, t1);
+        t0 = rcp_fast(t0);
+        t1 = rcp_fast(t1);
+        mul_rn_f32x2(u0, u1, u0, u1, e0, e1);
+        mul_rn_f32x2(e0, e1, -0.72134752044f, -0.72134752044f, e0, e1);  // log2(e) / 2
+        e0 = ex2_fast(e0);
+        e1 = ex2_fast(e1);
+        constexpr float kQ[9] = {-0.025177352130f, 0.13510350883f,   -0.26447525620f,
+                                 0.19280642271f,   -0.038633506745f, 0.11294532567f,
+                                 0.11576713622f,   0.13603937626f,   0.13562436402f};
+        q0 = q1 = kQ[0];
+#pragma unroll
+        for (int i = 1; i < 9; ++i) fma_rn_f32x2(q0, q1, t0, t1, kQ[i], kQ[i], q0, q1);
+        mul_rn_f32x2(q0, q1, t0, t1, q0, q1);
+        mul_rn_f32x2(q0, q1, e0, e1, q0, q1);  // Phi(-u)
+        fma_rn_f32x2(-u0, -u1, q0, q1, relu_nan(v0), relu_nan(v1), v0, v1);
+    }
+}
+
+// act on y[0..N), or, with kGates, on the values whose index has bit 1 clear
+// (the gates of a fragment, see epi_tile_channels).
+template <int kAct, bool kGates, int N>
+__device__ __forceinline__ void activate_values(float (&y)[N]) {
+#pragma unroll
+    for (int j = 0; j < N; j += 2)
+        if (!kGates || (j & 2) == 0) activate2<kAct>(y[j], y[j + 1]);
+}
+
+template <bool kGates, int N>
+__device__ __forceinline__ void activate(float (&y)[N], int act) {
+    switch (act) {
+        case kActRelu: activate_values<kActRelu, kGates>(y); break;
+        case kActSilu: activate_values<kActSilu, kGates>(y); break;
+        case kActGelu: activate_values<kActGelu, kGates>(y); break;
+        case kActGeluErf: activate_values<kActGeluErf, kGates>(y); break;
+        default: break;
     }
 }
 
 __device__ __forceinline__ float activate(float v, int act) {
-    switch (act) {
-        case kActRelu: return activate<kActRelu>(v);
-        case kActSilu: return activate<kActSilu>(v);
-        case kActGelu: return activate<kActGelu>(v);
-        case kActGeluErf: return activate<kActGeluErf>(v);
-        default: return v;
-    }
+    float y[2] = {v, 0.0f};
+    activate<false>(y, act);
+    return y[0];
 }
 
 __device__ __forceinline__ float load_f32_or_bf16(const void* p, int64_t i, int is_f32) {
@@ -81,34 +136,6 @@ __device__ __forceinline__ float epi_residual(const EpiArgs& e, int64_t off) {
 
 // Output column of weight row ch of a gated product (its gate rows).
 __device__ __forceinline__ int gated_col(int ch) { return ((ch >> 4) << 3) | (ch & 7); }
-
-// act on the fragment y[2][16] of a thread (see epi_tile_channels): every
-// value, or the gates (values 4 r + k).
-template <int kAct, bool kGates>
-__device__ __forceinline__ void activate_fragment(float (&y)[2][16]) {
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int j = 0; j < 16; ++j)
-            if (!kGates || (j & 2) == 0) y[h][j] = activate<kAct>(y[h][j]);
-}
-
-template <bool kGates>
-__device__ __forceinline__ void epi_activate(float (&y)[2][16], int act) {
-    switch (act) {
-        case kActRelu: activate_fragment<kActRelu, kGates>(y); break;
-        case kActSilu: activate_fragment<kActSilu, kGates>(y); break;
-        case kActGelu: activate_fragment<kActGelu, kGates>(y); break;
-        case kActGeluErf: activate_fragment<kActGeluErf, kGates>(y); break;
-        default: break;
-    }
-}
-__device__ __forceinline__ void epi_activate_all(float (&y)[2][16], int act) {
-    epi_activate<false>(y, act);
-}
-__device__ __forceinline__ void epi_activate_gates(float (&y)[2][16], int act) {
-    epi_activate<true>(y, act);
-}
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);

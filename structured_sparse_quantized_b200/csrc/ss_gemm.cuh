@@ -226,12 +226,13 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uin
     for (int u = 0; u < 32; ++u) {
         const float sb = __shfl_sync(0xffffffffu, sb_lane, u);
         const float acc = kInt8 ? __int2float_rn(static_cast<int32_t>(r[u])) : __uint_as_float(r[u]);
-        const float d = args.a_is_w ? __fmul_rn(__fmul_rn(acc, sb), sa)
-                                    : __fmul_rn(__fmul_rn(acc, sa), sb);
-        v[u] = d + (args.a_is_w ? bias_row : __shfl_sync(0xffffffffu, bias_lane, u));
+        v[u] = args.a_is_w
+                   ? fmaf(__fmul_rn(acc, sb), sa, bias_row)
+                   : fmaf(__fmul_rn(acc, sa), sb, __shfl_sync(0xffffffffu, bias_lane, u));
     }
     const int64_t row0 = args.a_is_w ? a_row : static_cast<int64_t>(a_row) * args.ldy;
     if (!e.gated) {
+        activate<false>(v, e.act);
         float res[32];  // every load is issued before the first store
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
@@ -243,26 +244,33 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uin
         for (int u = 0; u < 32; ++u) {
             const int b_row = b0 + u;
             const int64_t off = row0 + (args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy : b_row);
-            float y = activate(v[u], e.act);
+            float y = v[u];
             if (e.residual) y += res[u];
             if (row_ok && b_row < args.rowsB) store_y<kOutBf16>(args.y, off, y);
         }
     } else if (args.a_is_w) {  // the partner row is 8 lanes up
+        float up[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) up[u] = __shfl_down_sync(0xffffffffu, v[u], 8);
+        activate<false>(v, e.act);
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
             const int b_row = b0 + u;
-            const float y = activate(v[u], e.act) * __shfl_down_sync(0xffffffffu, v[u], 8);
+            const float y = v[u] * up[u];
             if (row_ok && (a_row & 8) == 0 && b_row < args.rowsB)
                 store_y<kOutBf16>(
                     args.y, static_cast<int64_t>(b_row) * args.ldy + gated_col(a_row), y);
         }
     } else {  // the partner column is this thread's
+        float g[16];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-            const int b_row = b0 + u;
-            if ((u & 8) == 0 && row_ok && b_row < args.rowsB)
-                store_y<kOutBf16>(args.y, row0 + gated_col(b_row),
-                                  activate(v[u], e.act) * v[(u + 8) & 31]);
+        for (int i = 0; i < 16; ++i) g[i] = v[((i & 8) << 1) | (i & 7)];
+        activate<false>(g, e.act);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int u = ((i & 8) << 1) | (i & 7);
+            if (row_ok && b0 + u < args.rowsB)
+                store_y<kOutBf16>(args.y, row0 + gated_col(b0 + u), g[i] * v[u + 8]);
         }
     }
 }
@@ -305,6 +313,13 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
     else return load_scale<kQ == kQBf16>(s, i, in_range);
 }
 
+// How a group of four epilogue warps walks its chunks of 32 B rows: chunk j of
+// a tile starts at column first + step j of the group's accumulator part, and
+// its tokens at tile * tile_b_rows + tok_off + that column.
+struct EpiWalk {
+    int first, step, per_tile, tok_off, tile_b_rows, tile_a_rows, nA, nB;
+};
+
 // The fused epilogue of one output tile for one group of four warps, A rows =
 // channels and bf16 Y by TMA: the transposed store path of gemm_kernel with
 // bias, activation and residual between the scaling and the rounding.
@@ -317,41 +332,52 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
 // The residual chunk comes by TMA into the staging buffer that the chunk of Y
 // leaves from, in the same swizzled layout: ldmatrix.trans gives a thread the
 // elements that its stmatrix.trans then overwrites, so nothing else is staged
-// and Y may be the residual.  The buffers alternate: while a chunk is worked
-// on, the next chunk's residual (of the next tile after the last) lands in the
-// other buffer, so that its latency is hidden by a whole chunk, or by the wait
-// for the next accumulator.
+// and Y may be the residual.  While a chunk is worked on, the residuals of the
+// next kBufs - 1 chunks (of the next tile after the last) land in the other
+// buffers.
 //
-// n: chunks this group has processed; issued: residual loads issued.  release
-// gives the accumulator back (one lane).  Returns false when a bounded wait
-// ran out (all four warps alike).
-template <typename C, int kQ, int kPair, typename Release>
+// One barrier per chunk: before it, the issuing thread has seen the store that
+// read the next chunk's buffer finish, so past it every warp may write there.
+//
+// kBatch chunks are read from tensor memory together: two where there is one
+// accumulator and a group has four chunks, which is then released after one
+// step of the loop (all four do not fit in registers beside the epilogue's).
+//
+// n: chunks this group has processed; issued: residual loads issued (issuer).
+// tile_at(i): the i-th tile of this cluster (>= n_tiles: none); release gives
+// the accumulator back (one lane).  Returns false when a bounded wait ran out
+// (all four warps alike).
+template <typename C, int kQ, int kBufs, int kBatch, typename TileAt, typename Release>
 __device__ __forceinline__ bool epi_tile_channels(
-    const GemmArgs& args, const CUtensorMap& tm_y, const CUtensorMap& tm_r, uint8_t* stage,
-    uint64_t* res_full, volatile int* abort_flag, uint32_t& n, uint32_t& issued, int unit,
-    int n_units, int n_tiles, int nA, int nB, int tile_a_rows, int a_cta0, int b0, int grp, int q,
-    int lane, bool issuer, uint32_t t_row, Release release) {
+    const GemmArgs& args, const EpiWalk& walk, const CUtensorMap& tm_y, const CUtensorMap& tm_r,
+    uint8_t* stage, uint64_t* res_full, volatile int* abort_flag, uint32_t& n, uint32_t& issued,
+    int n_tiles, int a_cta0, int b0, uint32_t grp_bar, int q, int lane, bool issuer,
+    uint32_t t_row, TileAt tile_at, Release release) {
     constexpr bool kInt8 = kQ == kQInt8;
+    static_assert(kBufs == 2 || kBufs == 4, "staging buffers");
     const EpiArgs& e = args.epi;
-    const uint32_t grp_bar = 1 + static_cast<uint32_t>(grp);
     const int t4 = lane >> 2, tm = lane & 3;
     const int mi = lane >> 3, mj = lane & 7;  // this thread's stmatrix matrix / row
-    // residual load of this group's chunk number j into buffer j & 1
-    const int per_tile = (args.bn - 32 * grp + 63) / 64;
+    // residual load of this group's chunk number j into buffer j % kBufs
     auto load_residual = [&](uint32_t j) {
-        const int tile = unit + static_cast<int>(j / per_tile) * n_units;
+        const int tile = tile_at(static_cast<int>(j / walk.per_tile));
         if (tile >= n_tiles) return;
         int ta, tb;
-        tile_coords(tile, nA, nB, args.a_groups, ta, tb);
-        const int ch = ta * tile_a_rows + a_cta0 % tile_a_rows;
-        const int tok = tb * args.bn + 32 * grp + 64 * static_cast<int>(j % per_tile);
-        uint8_t* dst = stage + (j & 1) * C::kEpiBytes;
-        mbar_arrive_expect_tx(&res_full[j & 1], C::kEpiBytes);
-        tma_load_2d(dst, &tm_r, &res_full[j & 1], ch, tok);
-        tma_load_2d(dst + 32 * 128, &tm_r, &res_full[j & 1], ch + 64, tok);
+        tile_coords(tile, walk.nA, walk.nB, args.a_groups, ta, tb);
+        const int ch = ta * walk.tile_a_rows + a_cta0 % walk.tile_a_rows;
+        const int tok = tb * walk.tile_b_rows + walk.tok_off + walk.first +
+                        walk.step * static_cast<int>(j % walk.per_tile);
+        uint8_t* dst = stage + (j % kBufs) * C::kEpiBytes;
+        mbar_arrive_expect_tx(&res_full[j % kBufs], C::kEpiBytes);
+        tma_load_2d(dst, &tm_r, &res_full[j % kBufs], ch, tok);
+        tma_load_2d(dst + 32 * 128, &tm_r, &res_full[j % kBufs], ch + 64, tok);
         issued = j + 1;
     };
-    if (args.tma_res && issuer && n == 0) load_residual(0);
+    // loads in flight ahead of the chunk worked on; with four buffers the one
+    // whose store was issued last is left alone
+    constexpr int kAhead = kBufs == 2 ? 1 : kBufs - 2;
+    if (args.tma_res && issuer && n == 0)
+        for (int j = 0; j < kAhead; ++j) load_residual(j);
     float sa2[2][2], bias2[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -362,97 +388,79 @@ __device__ __forceinline__ bool epi_tile_channels(
                                       : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
             bias2[h][x] = epi_bias(e, ch, ch < args.rowsA);
         }
-    // One accumulator: read the group's whole part before any of it is worked
-    // on, so that the next tile's MMAs can start.  Two: chunk by chunk.
-    constexpr int kCpg = (C::kBnMax + 63) / 64;
-    constexpr int kBatch = C::kAccBufs == 1 ? kCpg : 1;
 #pragma unroll 1
-    for (int cb = 0; cb < kCpg; cb += kBatch) {
+    for (int cb = 0; cb < walk.per_tile; cb += kBatch) {
         uint32_t v[kBatch][2][16];
 #pragma unroll
         for (int cc = 0; cc < kBatch; ++cc) {
-            const int c = 32 * grp + 64 * (cb + cc);
-            if (c < args.bn) {
+            const int c = walk.first + walk.step * (cb + cc);
+            if (cb + cc < walk.per_tile) {
                 tmem_ld_16x256b_x4(t_row + c, v[cc][0]);
                 tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[cc][1]);
             }
         }
+        // the token scales of the first chunk arrive while tensor memory is read
+        float sb[4][2];
+        auto load_sb = [&](int c) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int tok = b0 + c + 8 * r + 2 * tm;
+                if (kQ != kQNvfp4 && kQ != kQBf16 && tok + 1 < args.rowsB) {
+                    const float2 s = __ldg(reinterpret_cast<const float2*>(args.s_b + tok));
+                    sb[r][0] = s.x;
+                    sb[r][1] = s.y;
+                } else {
+                    sb[r][0] = load_b_scale<kQ>(args.s_b, tok, tok < args.rowsB);
+                    sb[r][1] = load_b_scale<kQ>(args.s_b, tok + 1, tok + 1 < args.rowsB);
+                }
+            }
+        };
+        load_sb(walk.first + walk.step * cb);
         tmem_ld_wait();
-        if (32 * grp + 64 * cb >= args.bn) break;
-        if (32 * grp + 64 * (cb + kBatch) >= args.bn) {  // last read: release
+        if (cb + kBatch >= walk.per_tile) {  // last read: release
             tc_fence_before();
             __syncwarp();
             if (lane == 0) release();
         }
 #pragma unroll
         for (int cc = 0; cc < kBatch; ++cc) {
-            const int c = 32 * grp + 64 * (cb + cc);
-            if (c >= args.bn) break;
-            uint8_t* buf = stage + (n & 1) * C::kEpiBytes;
+            if (cb + cc >= walk.per_tile) break;
+            const int c = walk.first + walk.step * (cb + cc);
+            if (cc > 0) load_sb(c);
+            uint8_t* buf = stage + (n % kBufs) * C::kEpiBytes;
             const uint32_t sy = smem_u32(buf);
             if (args.tma_res && issuer) {
-                bulk_wait_read<0>();  // the previous chunk has left the other buffer
-                load_residual(n + 1);
+                bulk_wait_read<kBufs == 2 ? 0 : 1>();
+                load_residual(n + kAhead);
             }
-            float y[2][16];  // [h][4 r + 2 x + k]
-            float sb[4][2];
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int tok = b0 + c + 8 * r + 2 * tm + k;
-                    sb[r][k] = load_b_scale<kQ>(args.s_b, tok, tok < args.rowsB);
-                }
+            float y[32];  // [16 h + 4 r + 2 x + k]
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const uint32_t bits = v[cc][h][j];
-                    const float acc =
-                        kInt8 ? __int2float_rn(static_cast<int32_t>(bits)) : __uint_as_float(bits);
+                for (int j = 0; j < 16; j += 2) {
+                    const uint32_t b0_ = v[cc][h][j], b1_ = v[cc][h][j + 1];
+                    const float x0 = kInt8 ? __int2float_rn(static_cast<int32_t>(b0_))
+                                           : __uint_as_float(b0_);
+                    const float x1 = kInt8 ? __int2float_rn(static_cast<int32_t>(b1_))
+                                           : __uint_as_float(b1_);
                     const int x = (j >> 1) & 1;
-                    y[h][j] = __fmul_rn(__fmul_rn(acc, sb[j >> 2][j & 1]), sa2[h][x]) + bias2[h][x];
+                    float &y0 = y[16 * h + j], &y1 = y[16 * h + j + 1];
+                    mul_rn_f32x2(x0, x1, sb[j >> 2][0], sb[j >> 2][1], y0, y1);
+                    fma_rn_f32x2(y0, y1, sa2[h][x], sa2[h][x], bias2[h][x], bias2[h][x], y0, y1);
                 }
-            uint32_t pk[2][8];
             bool got = true;
             if (e.gated) {
-                epi_activate_gates(y, e.act);
+                activate<true>(y, e.act);
+                uint32_t pk[2][4];
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        pk[h][r] = pack_bf16(y[h][4 * r] * y[h][4 * r + 2],
-                                             y[h][4 * r + 1] * y[h][4 * r + 3]);
-            } else {
-                epi_activate_all(y, e.act);
-                if (args.tma_res) {
-                    got = mbar_wait(&res_full[n & 1], (n >> 1) & 1, abort_flag);
-                    __syncwarp();
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int rp = 0; rp < 2; ++rp) {
-                        uint32_t rr[4] = {0u, 0u, 0u, 0u};
-                        if (args.tma_res)
-                            ldmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), rr);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int i = 8 * rp + 2 * j;
-                            float y0 = y[h][i], y1 = y[h][i + 1];
-                            if (args.tma_res) {
-                                y0 += __uint_as_float(rr[j] << 16);
-                                y1 += __uint_as_float(rr[j] & 0xFFFF0000u);
-                            }
-                            pk[h][4 * rp + j] = pack_bf16(y0, y1);
-                        }
+                    for (int r = 0; r < 4; ++r) {
+                        const int i = 16 * h + 4 * r;
+                        float y0, y1;
+                        mul_rn_f32x2(y[i], y[i + 1], y[i + 2], y[i + 3], y0, y1);
+                        pk[h][r] = pack_bf16(y0, y1);
                     }
-            }
-            if (!args.tma_res) {  // the store of two chunks ago has left this buffer
-                if (issuer) bulk_wait_read<1>();
-                named_bar_sync(grp_bar, 128);
-            }
-            if (e.gated) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3
@@ -460,15 +468,38 @@ __device__ __forceinline__ bool epi_tile_channels(
                                       pk[h][1], pk[h][2], pk[h][3]);
                 }
             } else {
+                activate<false>(y, e.act);
+                if (args.tma_res) {
+                    got = mbar_wait(&res_full[n % kBufs], (n / kBufs) & 1, abort_flag);
+                    __syncwarp();
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int rp = 0; rp < 2; ++rp) {
+                            uint32_t rr[4];
+                            ldmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), rr);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                const int i = 16 * h + 8 * rp + 2 * j;
+                                add_rn_f32x2(y[i], y[i + 1], __uint_as_float(rr[j] << 16),
+                                             __uint_as_float(rr[j] & 0xFFFF0000u), y[i], y[i + 1]);
+                            }
+                        }
+                }
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int rp = 0; rp < 2; ++rp)
-                        stmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), pk[h][4 * rp],
-                                          pk[h][4 * rp + 1], pk[h][4 * rp + 2],
-                                          pk[h][4 * rp + 3]);
+                    for (int rp = 0; rp < 2; ++rp) {
+                        const int i = 16 * h + 8 * rp;
+                        stmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj),
+                                          pack_bf16(y[i], y[i + 1]), pack_bf16(y[i + 2], y[i + 3]),
+                                          pack_bf16(y[i + 4], y[i + 5]),
+                                          pack_bf16(y[i + 6], y[i + 7]));
+                    }
             }
             fence_async_shared();
+            // the store that read the next chunk's buffer is done (n - 1 or n - 3)
+            if (issuer) bulk_wait_read<kBufs - 2>();
             if (!named_bar_and(grp_bar, 128, got)) return false;
             if (issuer) {
                 const uint64_t stream = l2_policy_evict_first();
@@ -868,10 +899,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             if constexpr (kEpi && kOutBf16) {
                 if (args.tma_store && args.a_is_w) {
                     // as the path below, with the fused epilogue
-                    if (!epi_tile_channels<C, kQ, kPair>(
-                            args, tm_y, tm_r, sy, &res_full[2 * grp], abort_flag, epi_n, epi_issued,
-                            unit, n_units, n_tiles, nA, nB, tile_a_rows, a_cta0, b0, grp, q, lane,
-                            issuer, t_row, [&] {
+                    const EpiWalk walk = {32 * grp, 64,  (args.bn - 32 * grp + 63) / 64, 0,
+                                          args.bn,  tile_a_rows, nA, nB};
+                    if (!epi_tile_channels<C, kQ, C::kEpiBufs / 2, C::kAccBufs == 1 ? 2 : 1>(
+                            args, walk, tm_y, tm_r, sy, &res_full[2 * grp], abort_flag, epi_n,
+                            epi_issued, n_tiles, a_cta0, b0, grp_bar, q, lane, issuer, t_row,
+                            [&](int j) { return unit + j * n_units; },
+                            [&] {
                                 if constexpr (kPair == 2)
                                     mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
                                 else

@@ -255,7 +255,8 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
         const int et = threadIdx.x - 64;  // 0..127
         uint32_t peer[8];
         for (int p = 0; p < S; ++p) peer[p] = map_to_rank(part, static_cast<uint32_t>(p));
-        // the dequantised sum of the parts at (row rl of this slice, column col)
+        // the dequantised sum of the parts at (row rl of this slice, column col),
+        // plus the fused epilogue's bias
         auto dequant = [&](int rl, int col) {
             const uint32_t off = static_cast<uint32_t>((col * kTileA + r0 + rl) * 4);
             float accv;
@@ -277,7 +278,9 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
             }
             const float sa = load_scale<kBf16>(args.s_a, a0 + r0 + rl, true);
             const float sb = load_scale<kBf16>(args.s_b, col, true);
-            return __fmul_rn(__fmul_rn(accv, sb), sa);
+            const float d = __fmul_rn(accv, sb);
+            if constexpr (kEpi) return fmaf(d, sa, epi_bias(args.epi, a0 + r0 + rl, true));
+            else return __fmul_rn(d, sa);
         };
         if (kEpi && args.epi.gated) {  // a slice is whole 16-row groups: both factors are here
             for (int f = et; f < rows / 2 * args.bn; f += 128) {
@@ -285,8 +288,7 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
                 const int rl = ((i >> 3) << 4) | (i & 7);
                 const int ch = a0 + r0 + rl;
                 if (ch >= args.rowsA || col >= args.rowsB) continue;
-                const float g = dequant(rl, col) + epi_bias(args.epi, ch, true);
-                const float u = dequant(rl + 8, col) + epi_bias(args.epi, ch + 8, true);
+                const float g = dequant(rl, col), u = dequant(rl + 8, col);
                 store_y<kOutBf16>(args.y, static_cast<int64_t>(col) * args.ldy + gated_col(ch),
                                   activate(g, args.epi.act) * u);
             }
@@ -299,7 +301,7 @@ __global__ void __launch_bounds__(kSplitKThreads, 1)
                 float y = dequant(rl, col);
                 const int64_t o = static_cast<int64_t>(tok) * args.ldy + ch;
                 if constexpr (kEpi) {
-                    y = activate(y + epi_bias(args.epi, ch, true), args.epi.act);
+                    y = activate(y, args.epi.act);
                     if (args.epi.residual) y += epi_residual(args.epi, o);
                 }
                 store_y<kOutBf16>(args.y, o, y);

@@ -46,6 +46,7 @@ namespace ss {
 constexpr int kWideThreads = 320;  // warp 0 producer, warp 1 MMA, warps 2-9 epilogue
 constexpr int kWideBT = 2;         // B tiles per output tile
 
+template <bool kEpi = false>
 struct WideCfg {
     static constexpr int kStageK = 128;                   // logical K per stage
     static constexpr int kARowBytes = kStageK / 2;        // 64 compressed bytes
@@ -58,7 +59,10 @@ struct WideCfg {
     static constexpr int kEOffset = kBOffset + kWideBT * kBTileBytes;
     static constexpr int kStageBytes = (kEOffset + kEBytes + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;     // one [32 tokens][128 channels] chunk
-    static constexpr int kEpiGroupBytes = 2 * kEpiBytes;  // double buffer per B tile
+    // Y chunks staged per B tile: two, or with the fused epilogue four, so that
+    // two residual chunks are on their way while one is worked on
+    static constexpr int kEpiBufs = kEpi ? 4 : 2;
+    static constexpr int kEpiGroupBytes = kEpiBufs * kEpiBytes;
     static constexpr int kBarBytes = 256;
     static constexpr int kStages =
         (227 * 1024 - 1024 - kBarBytes - 64 - kWideBT * kBnMax * 4 - kWideBT * kEpiGroupBytes) /
@@ -86,13 +90,19 @@ __device__ __forceinline__ int snake_tile(int k, int unit, int n_units) {
 
 // kAIsW: A rows are output channels (weight-sparse, Y[b, a]); otherwise A
 // rows are tokens (activation-sparse, Y[a, b]).
-template <bool kInt8, bool kAIsW>
+// kEpi (kAIsW only): the fused epilogue of args.epi (ss_epilogue.cuh; tm_r is
+// the residual's map).  A group then takes its accumulator chunk by chunk
+// (epi_tile_channels) instead of holding it as packed bf16: what the bias, the
+// activation and the residual are added to is not rounded yet.
+template <bool kInt8, bool kAIsW, bool kEpi = false>
 __global__ void __launch_bounds__(kWideThreads, 1)
     gemm_sparse_wide_kernel(const __grid_constant__ CUtensorMap tm_a,
                             const __grid_constant__ CUtensorMap tm_b,
                             const __grid_constant__ CUtensorMap tm_e,
-                            const __grid_constant__ CUtensorMap tm_y, const GemmArgs args) {
-    using C = WideCfg;
+                            const __grid_constant__ CUtensorMap tm_y,
+                            const __grid_constant__ CUtensorMap tm_r, const GemmArgs args) {
+    using C = WideCfg<kEpi>;
+    static_assert(kAIsW || !kEpi, "the fused epilogue takes channel rows");
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -101,7 +111,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint64_t* acc_full = empty + C::kStages;
     uint64_t* acc_empty = acc_full + 1;
     uint64_t* drain = acc_empty + 1;
-    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    uint64_t* res_full = drain + 1;  // [2 B tiles][kEpiBufs]: a residual chunk has landed (kEpi)
+    uint32_t* tmem_base_slot =
+        reinterpret_cast<uint32_t*>(res_full + (kEpi ? kWideBT * C::kEpiBufs : 0));
     __shared__ int abort_flag_storage;
     volatile int* abort_flag = &abort_flag_storage;
     pdl_trigger();
@@ -128,6 +140,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         mbar_init(acc_full, 1);
         mbar_init(acc_empty, 8 * 2);  // 8 epilogue warps in each CTA of the pair
         mbar_init(drain, 1);
+        for (int b = 0; kEpi && b < kWideBT * C::kEpiBufs; ++b) mbar_init(&res_full[b], 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -311,6 +324,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int mi = lane >> 3, mj = lane & 7;  // this thread's stmatrix matrix / row
         int i = 0;
         uint32_t chunk_iter = 0;
+        [[maybe_unused]] uint32_t epi_n = 0, epi_issued = 0;
         for (int t = snake_tile(0, unit, n_units); t < n_tiles;
              ++i, t = snake_tile(i, unit, n_units)) {
             int ta, tb_;
@@ -318,6 +332,22 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int a_cta0 = ta * kPairRows + static_cast<int>(rank) * kTileA;
             const int tile_tok0 = tb_ * tile_b_rows;
             const int tok0 = tile_tok0 + bt * args.bn;
+            if constexpr (kEpi) {
+                const bool ready = mbar_wait(acc_full, static_cast<uint32_t>(i & 1), abort_flag);
+                if (!named_bar_and(grp_bar, 128, ready)) break;
+                tc_fence_after();
+                const EpiWalk walk = {0, 32, args.bn / 32, bt * args.bn, tile_b_rows, kPairRows,
+                                      nA, nB};
+                const bool done = epi_tile_channels<C, kInt8 ? kQInt8 : kQE4M3, C::kEpiBufs, 1>(
+                    args, walk, tm_y, tm_r, stage_y, &res_full[C::kEpiBufs * bt], abort_flag,
+                    epi_n, epi_issued, n_tiles, a_cta0, tok0, grp_bar, q, lane, issuer,
+                    tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
+                        static_cast<uint32_t>(bt * C::kAccStride),
+                    [&](int j) { return snake_tile(j, unit, n_units); },
+                    [&] { mbar_arrive_cluster(acc_empty_leader); });
+                if (!done) break;
+                continue;
+            }
             // scales of this tile, fetched while its MMAs still run
             float sb_pre[2];
 #pragma unroll
@@ -474,6 +504,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     ++chunk_iter;
                 }
             }
+        }
+        if constexpr (kEpi) {  // after a wait that ran out: residual loads in flight land
+            for (; issuer && epi_n < epi_issued; ++epi_n)
+                mbar_drain(&res_full[C::kEpiBufs * bt + epi_n % C::kEpiBufs],
+                           (epi_n / C::kEpiBufs) & 1);
         }
         if (issuer) bulk_wait_all();  // Y stores done reading shared memory
     }

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
     const T* __restrict__ X, const void* __restrict__ w, int wf32, float eps, int64_t M,
     const NormShape s, int slot_stride, int q_stride, uint8_t* __restrict__ Xq,
     float* __restrict__ s_x) {
-    extern __shared__ __align__(128) uint8_t smem_raw[];
+    extern __shared__ __align__(16) uint8_t smem_raw[];
     constexpr int kSets = kWarpRowThreads / (32 * kWpr);
     __shared__ uint64_t full[kSets][kNormSlots];
     __shared__ float2 part[2][kSets][kWpr];

@@ -64,25 +64,31 @@ def operand_fp4(rng, rows, L, sparse, block):
 
 
 def dequantised(x, w, s_x, s_w):
-    """((float)acc * s_x) * s_w in fp32; the accumulator is exact."""
+    """(float)acc * s_x in fp32 (the accumulator is exact), times s_w in 64 bits:
+    v of the epilogue before the bias and the one rounding of their sum."""
     acc = (x @ w.T).astype(np.float32)
     if s_x is None:
-        return acc
-    return (acc * np.asarray(s_x, np.float32).reshape(-1, 1)) * np.asarray(s_w, np.float32)
+        return acc.astype(np.float64)
+    d = acc * np.asarray(s_x, np.float32).reshape(-1, 1)
+    return d.astype(np.float64) * np.asarray(s_w, np.float32).astype(np.float64)
 
 
 def activate(v, act):
     """act(v) in 64 bits, and a bound on the kernel's relative error against it
-    for an fp32 v that is off by half a unit in the last place.
+    for an fp32 v that is off by half a unit in the last place (units of 2^-23).
 
-    __expf(x) is off by at most 2 + 1.173 |x| units of 2^-23 (its documented
-    bound), __fdividef by 2 units, the fp32 sum by half.  silu: the exponent is
-    -v itself, and v's own half unit moves e^-v by |v| half units: 7 + 2 |v|
-    units in all, rounded up.  gelu: the exponent u2 = 2 sqrt(2/pi) (v +
-    0.044715 v^3) carries 3 roundings (1.5 |u2| units in e^-u2), and v's half
-    unit changes it by at most 3 |u2| / 2: 8 + 5 |u2| units.  gelu_erf: erfcf is
-    off by at most 4 units, its argument z by 1.5 half units plus v's, each
-    acting 2 z^2 = v^2 fold for large z: 6 + 2 v^2 units."""
+    2^x and 1/x are off by at most 2 units and 1 unit (their documented bounds),
+    every product or sum by half.  silu: the exponent -v log2 e carries 1 unit
+    of itself (its constant's rounding and the product's), i.e. |v| units in
+    e^-v, and v's own half unit |v| / 2 more: 2 + 1.5 |v|, then 1/2 + 1 + 1/2:
+    below 7 + 2 |v|.  gelu: the exponent u2 = 2 sqrt(2/pi) (v + 0.044715 v^3)
+    carries 2.5 units (two constants, three operations), and v's half unit
+    changes it by at most 3 |u2| / 2 units: below 8 + 5 |u2|.  gelu_erf: with
+    u = |v|, Phi(-u) = e^(-u^2 / 2) t Q(t): 2.7 units for the polynomial in fp32,
+    1 for the reciprocal t (the product t Q changes less than t does), 2 and
+    1.5 u^2 / 2 for the power, 1.5 for the products, u^2 / 2 for v's half unit
+    (and 1/2 in the factor v): 7.7 + 1.25 u^2, rounded up to 9 + 2 v^2; for v > 0
+    it enters with a factor below 1."""
     if act == "relu":
         return np.where(v < 0, 0.0, v), np.full_like(v, ULP)
     if act == "silu":
@@ -93,7 +99,7 @@ def activate(v, act):
         return v / (1 + np.exp(np.minimum(-u2, 700.0))), (8 + 5 * np.abs(u2)) * ULP
     if act == "gelu_erf":
         phi = 0.5 * torch.special.erfc(torch.from_numpy(-v / np.sqrt(2.0))).numpy()
-        return v * phi, (6 + 2 * v * v) * ULP
+        return v * phi, (9 + 2 * v * v) * ULP
     return v, np.full_like(v, ULP / 2)
 
 
@@ -102,8 +108,8 @@ def half_step(out):
 
 
 def epilogue(d, bias, act, gated, residual, out):
-    """(the epilogue of the fp32 matrix d in 64 bits, bound on |Y - that|)."""
-    v = d.astype(np.float64)
+    """(the epilogue of dequantised()'s d in 64 bits, bound on |Y - that|)."""
+    v = d
     if bias is not None:
         v = v + bias.double().numpy()
     if gated:

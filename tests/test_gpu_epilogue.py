@@ -159,7 +159,7 @@ def test_empty_epilogue_equals_plain_call():
     for tier, form in FORMS:
         p = Product(130, 144, 256, tier, form)
         y = p.run(ss.Epilogue(), BF)
-        want = torch.from_numpy(p.d).to(BF)
+        want = torch.from_numpy(p.d).float().to(BF)  # the fp32 value, then bf16
         assert torch.equal(y.cpu(), want)
 
 
