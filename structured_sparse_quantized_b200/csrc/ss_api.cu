@@ -150,7 +150,7 @@ bool make_map_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t col
 // box [32 tokens][128 channels] when A rows are channels, [128 tokens][32
 // channels] otherwise.  Returns false (direct stores instead) when the rows
 // of Y are not 16-byte aligned.
-bool make_y_map(CUtensorMap* map, const void* Y, int64_t M, int64_t N, bool out_bf16, bool a_is_w) {
+bool make_y_map(CUtensorMap* map, void* Y, int64_t M, int64_t N, bool out_bf16, bool a_is_w) {
     const uint32_t esz = out_bf16 ? 2 : 4;
     if (!out_bf16 || (N * esz) % 16 != 0) return false;  // fp32 Y: direct stores
     const CUtensorMapDataType dt =
@@ -182,7 +182,8 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
         ((args.rowsA + tile_rows - 1) / tile_rows) * ((args.rowsB + args.bn - 1) / args.bn);
     const int64_t units = g_num_sms[dev] / kPair;
     const int grid = static_cast<int>((tiles < units ? tiles : units) * kPair);
-    return launch_ex(kern, dim3(grid), dim3(ss::kGemmThreads), C::kSmemBytes, stream, kPair, a, b,
+    return launch_ex(kern, dim3(grid), dim3(kEpi ? ss::kFusedThreads : ss::kGemmThreads),
+                     C::kSmemBytes, stream, kPair, a, b,
                      e, y, sfa ? *sfa : a, sfb ? *sfb : a, r, args);
 }
 
@@ -215,18 +216,27 @@ ss_status dispatch_gemm_any(int dev, int q, bool bf16, int pair, bool fused, con
 
 // Maps and paths of Y and the residual (N columns of Y; A rows = channels or
 // not): sets args.tma_store and args.tma_res; unused maps are copies of `any`.
+// A fused epilogue takes the TMA path for bf16 Y and channel rows, unless the
+// residual is fp32; its warps store boxes of 32 tokens x 32 channels (16 of a
+// gated product).
 void epilogue_maps(const CUtensorMap& any, void* Y, int64_t M, int64_t N, bool bf16, bool fused,
                    ss::GemmArgs* args, CUtensorMap* y, CUtensorMap* r) {
     *y = *r = any;
     args->tma_res = 0;
-    args->tma_store = make_y_map(y, Y, M, N, bf16, args->a_is_w) ? 1 : 0;
-    if (!fused || !args->tma_store) return;
-    // a fused epilogue takes the TMA path for channel rows, unless the residual
-    // is fp32
-    if (!args->a_is_w || args->epi.res_f32) {
-        args->tma_store = 0;
-    } else if (args->epi.residual) {
-        args->tma_res = make_y_map(r, args->epi.residual, M, N, true, true) ? 1 : 0;
+    if (!fused) {
+        args->tma_store = make_y_map(y, Y, M, N, bf16, args->a_is_w) ? 1 : 0;
+        return;
+    }
+    auto box = [&](CUtensorMap* map, const void* base) {
+        const bool gated = args->epi.gated;
+        return make_map_2d(map, base, M, N, 32, gated ? 16 : 32,
+                           gated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
+    };
+    args->tma_store =
+        bf16 && args->a_is_w && N % 8 == 0 && !args->epi.res_f32 && box(y, Y) ? 1 : 0;
+    if (args->tma_store && args->epi.residual) {
+        args->tma_res = box(r, args->epi.residual) ? 1 : 0;
         args->tma_store = args->tma_res;
     }
 }
@@ -378,7 +388,8 @@ ss_status launch_gemm_wide(int dev, const CUtensorMap& a, const CUtensorMap& b,
                           ((args.rowsB + tile_b - 1) / tile_b);
     const int64_t units = g_num_sms[dev] / 2;
     const int grid = static_cast<int>((tiles < units ? tiles : units) * 2);
-    return launch_ex(kern, dim3(grid), dim3(ss::kWideThreads), C::kSmemBytes, stream, 2, a, b, e,
+    return launch_ex(kern, dim3(grid), dim3(kEpi ? ss::kFusedThreads : ss::kWideThreads),
+                     C::kSmemBytes, stream, 2, a, b, e,
                      y, r, args);
 }
 

@@ -142,16 +142,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Address of this thread's row of the four 8x8 blocks (r = 2 rp, 2 rp + 1) x
-// (channel blocks e = 0, 1) in a staged [2 halves][32 tokens][64 channels]
-// chunk with 128B swizzle.
-__device__ __forceinline__ uint32_t epi_block_addr(uint32_t base, int rp, int q, int h, int mi,
-                                                   int mj) {
-    const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
-    const int ch = q * 32 + 16 * h + 8 * (mi & 1);
-    return base + (ch >> 6) * (32 * 128) + tok * 128 + ((((ch & 63) >> 3) ^ (tok & 7)) << 4);
-}
-
 template <bool kOutBf16>
 __device__ __forceinline__ void store_y(void* y, int64_t off, float v) {
     if constexpr (kOutBf16)

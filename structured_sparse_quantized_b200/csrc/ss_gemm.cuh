@@ -50,6 +50,14 @@ namespace ss {
 
 constexpr int kGemmEpiWarps = 8;  // two groups of four, one warp per TMEM lane quarter each
 constexpr int kGemmThreads = 64 + 32 * kGemmEpiWarps;
+// With the fused epilogue four groups: its arithmetic keeps a group of four
+// warps (one per scheduler) at well under one instruction a cycle, and what it
+// takes for the last tile, or for every tile of a single-buffered accumulator,
+// is not hidden behind MMAs (8192 x 4096 x 4096 2:4 INT8 with SiLU: two groups
+// 74 us, plain product 63).
+constexpr int kFusedEpiWarps = 16;
+constexpr int kFusedThreads = 64 + 32 * kFusedEpiWarps;
+constexpr int kFusedWarpBytes = 2048;  // one warp's 32 tokens x 32 channels of bf16
 constexpr int kL2PrefetchStages = 16;  // weight stages a CTA prefetches before pdl_wait
 constexpr int kTileA = 128;  // A rows per CTA per A tile
 constexpr int kTmemCols = 512;
@@ -85,11 +93,11 @@ struct GemmCfg {
     static constexpr int kStageRaw = kEOffset + kEBytes;
     static constexpr int kStageBytes = (kStageRaw + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;      // one 32-column bf16 chunk of Y
-    // staging buffers for Y chunks: one per epilogue group, or two where the
-    // fused epilogue loads the residual of the next chunk into the other one
+    // staging buffers for Y chunks: one per epilogue group
     static constexpr int kEpiBufs = kEpi ? 4 : 2;
+    static constexpr int kBarBytes = kEpi ? 512 : 256;
     static constexpr int kSmemBudget =
-        (kEpi ? 226 : 225) * 1024 - 1024 - 256 - kEpiBufs * kEpiBytes;
+        (kEpi ? 226 : 225) * 1024 - 1024 - kBarBytes - kEpiBufs * kEpiBytes;
     static constexpr int kStagesRaw = kSmemBudget / kStageBytes;
     static constexpr int kStages = kStagesRaw > 8 ? 8 : kStagesRaw;
     static constexpr int kAccBufs = 2;                     // accumulators in TMEM
@@ -102,14 +110,14 @@ struct GemmCfg {
     static constexpr int kESlots = kStages;
     static constexpr int kEpiOffset = kStages * kStageBytes;
     static constexpr int kSmemBytes =
-        kEpiOffset + kEpiBufs * kEpiBytes + 1024 /*align*/ + 256 /*barriers*/;
+        kEpiOffset + kEpiBufs * kEpiBytes + 1024 /*align*/ + kBarBytes;
     static_assert(kABytes % 1024 == 0 && kBAtomBytes % 1024 == 0, "tile alignment");
     static_assert(kARowBytes == 128 && kMmaPerStage == 4, "stage geometry");
     static_assert(!kSparse || kECol + kESlots * kESlotCols <= kTmemCols, "TMEM budget");
     static_assert(kECol % 2 == 0 && kESlotCols % 2 == 0, "metadata column pairs stay aligned");
     static_assert(kSmemBytes <= 227 * 1024, "shared memory budget");
     static_assert(kStages >= (kPair == 2 ? 3 : 2), "pipeline depth");
-    static_assert((2 * kStages + 9) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 5 + (kEpi ? 16 : 0)) * 8 + 4 <= kBarBytes, "barrier area");
 };
 
 // Stage layout of the block-scaled FP4 GEMM: per stage 4 MMAs (sparse: K =
@@ -154,8 +162,9 @@ struct Fp4Cfg {
     static constexpr int kStageBytes = (kSfbOffset + kSfbBytes + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;
     static constexpr int kEpiBufs = kEpi ? 4 : 2;
+    static constexpr int kBarBytes = kEpi ? 512 : 256;
     static constexpr int kSmemBudget =
-        (kEpi ? 226 : 225) * 1024 - 1024 - 256 - kEpiBufs * kEpiBytes;
+        (kEpi ? 226 : 225) * 1024 - 1024 - kBarBytes - kEpiBufs * kEpiBytes;
     static constexpr int kStagesRaw = kSmemBudget / kStageBytes;
     static constexpr int kESlotCols = 4 * kEChunks;
     static constexpr int kSfaCols = 4 * kMmaPerStage;
@@ -170,10 +179,10 @@ struct Fp4Cfg {
     static constexpr int kESlots = kStages;
     static constexpr int kSfCol = kECol + kStages * kESlotCols;  // scale slots
     static constexpr int kEpiOffset = kStages * kStageBytes;
-    static constexpr int kSmemBytes = kEpiOffset + kEpiBufs * kEpiBytes + 1024 + 256;
+    static constexpr int kSmemBytes = kEpiOffset + kEpiBufs * kEpiBytes + 1024 + kBarBytes;
     static_assert(kSfCol % 4 == 0 && kSfCol + kSfSlotCols * kStages <= kTmemCols, "TMEM budget");
     static_assert(kSmemBytes <= 227 * 1024 && kStages >= 3, "shared memory budget");
-    static_assert((2 * kStages + 9) * 8 + 4 <= 256, "barrier area");
+    static_assert((2 * kStages + 5 + (kEpi ? 16 : 0)) * 8 + 4 <= kBarBytes, "barrier area");
 };
 
 struct GemmArgs {
@@ -209,69 +218,62 @@ __device__ __forceinline__ void store_scaled(void* y, int64_t off, uint32_t acc_
         reinterpret_cast<float*>(y)[off] = v;
 }
 
-// Epilogue of one thread's accumulator row (a_row, columns b0 .. b0 + 31)
-// straight to global memory; sa is the row's scale, sb_lane the scale of
-// column b0 + lane.
+// Epilogue of one thread's accumulator row (a_row, columns b0 .. b0 + 15)
+// straight to global memory; sa is the row's scale, sb_lane and bias_lane the
+// scale and (token rows) the bias of column b0 + lane % 16, bias_row the bias
+// of a channel row.
 template <bool kInt8, bool kOutBf16>
-__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uint32_t (&r)[32],
-                                                 int a_row, int b0, int lane, float sa,
-                                                 float sb_lane) {
+__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uint32_t (&r)[16],
+                                                 int a_row, int b0, float sa, float sb_lane,
+                                                 float bias_row, float bias_lane) {
     const EpiArgs& e = args.epi;
     const bool row_ok = a_row < args.rowsA;
-    const float bias_row = args.a_is_w ? epi_bias(e, a_row, row_ok) : 0.0f;
-    const float bias_lane =
-        args.a_is_w ? 0.0f : epi_bias(e, b0 + lane, b0 + lane < args.rowsB);
-    float v[32];
+    float v[16];
 #pragma unroll
-    for (int u = 0; u < 32; ++u) {
+    for (int u = 0; u < 16; ++u) {
         const float sb = __shfl_sync(0xffffffffu, sb_lane, u);
         const float acc = kInt8 ? __int2float_rn(static_cast<int32_t>(r[u])) : __uint_as_float(r[u]);
         v[u] = args.a_is_w
                    ? fmaf(__fmul_rn(acc, sb), sa, bias_row)
                    : fmaf(__fmul_rn(acc, sa), sb, __shfl_sync(0xffffffffu, bias_lane, u));
     }
-    const int64_t row0 = args.a_is_w ? a_row : static_cast<int64_t>(a_row) * args.ldy;
+    // element u is at off0 + u * stride of Y (and of the residual)
+    const int64_t stride = args.a_is_w ? args.ldy : 1;
+    const int n = row_ok ? min(16, args.rowsB - b0) : 0;
     if (!e.gated) {
+        const int64_t off0 = args.a_is_w ? static_cast<int64_t>(b0) * args.ldy + a_row
+                                         : static_cast<int64_t>(a_row) * args.ldy + b0;
         activate<false>(v, e.act);
-        float res[32];  // every load is issued before the first store
+        if (e.residual) {
+            float res[16];  // every load is issued before the first store
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-            const int b_row = b0 + u;
-            const int64_t off = row0 + (args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy : b_row);
-            res[u] = e.residual && row_ok && b_row < args.rowsB ? epi_residual(e, off) : 0.0f;
+            for (int u = 0; u < 16; ++u)
+                res[u] = u < n ? epi_residual(e, off0 + u * stride) : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) v[u] += res[u];
         }
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-            const int b_row = b0 + u;
-            const int64_t off = row0 + (args.a_is_w ? static_cast<int64_t>(b_row) * args.ldy : b_row);
-            float y = v[u];
-            if (e.residual) y += res[u];
-            if (row_ok && b_row < args.rowsB) store_y<kOutBf16>(args.y, off, y);
-        }
+        for (int u = 0; u < 16; ++u)
+            if (u < n) store_y<kOutBf16>(args.y, off0 + u * stride, v[u]);
     } else if (args.a_is_w) {  // the partner row is 8 lanes up
-        float up[32];
+        float up[16];
 #pragma unroll
-        for (int u = 0; u < 32; ++u) up[u] = __shfl_down_sync(0xffffffffu, v[u], 8);
+        for (int u = 0; u < 16; ++u) up[u] = __shfl_down_sync(0xffffffffu, v[u], 8);
         activate<false>(v, e.act);
+        const int64_t off0 = static_cast<int64_t>(b0) * args.ldy + gated_col(a_row);
 #pragma unroll
-        for (int u = 0; u < 32; ++u) {
-            const int b_row = b0 + u;
-            const float y = v[u] * up[u];
-            if (row_ok && (a_row & 8) == 0 && b_row < args.rowsB)
-                store_y<kOutBf16>(
-                    args.y, static_cast<int64_t>(b_row) * args.ldy + gated_col(a_row), y);
-        }
-    } else {  // the partner column is this thread's
-        float g[16];
+        for (int u = 0; u < 16; ++u)
+            if (u < n && (a_row & 8) == 0)
+                store_y<kOutBf16>(args.y, off0 + u * stride, v[u] * up[u]);
+    } else {  // the partner column is this thread's; N is a multiple of 16
+        float g[8];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) g[i] = v[((i & 8) << 1) | (i & 7)];
+        for (int u = 0; u < 8; ++u) g[u] = v[u];
         activate<false>(g, e.act);
+        const int64_t off0 = static_cast<int64_t>(a_row) * args.ldy + gated_col(b0);
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int u = ((i & 8) << 1) | (i & 7);
-            if (row_ok && b0 + u < args.rowsB)
-                store_y<kOutBf16>(args.y, row0 + gated_col(b0 + u), g[i] * v[u + 8]);
-        }
+        for (int u = 0; u < 8; ++u)
+            if (u < n) store_y<kOutBf16>(args.y, off0 + u, g[u] * v[u + 8]);
     }
 }
 
@@ -313,208 +315,194 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
     else return load_scale<kQ == kQBf16>(s, i, in_range);
 }
 
-// How a group of four epilogue warps walks its chunks of 32 B rows: chunk j of
-// a tile starts at column first + step j of the group's accumulator part, and
-// its tokens at tile * tile_b_rows + tok_off + that column.
+// How a warp of the fused epilogue walks a tile's chunks of 32 B rows: chunk j
+// starts at column first + step j of the warp's accumulator part, and its
+// tokens at tile * tile_b_rows + tok_off + that column.
 struct EpiWalk {
     int first, step, per_tile, tok_off, tile_b_rows, tile_a_rows, nA, nB;
 };
 
-// The fused epilogue of one output tile for one group of four warps, A rows =
-// channels and bf16 Y by TMA: the transposed store path of gemm_kernel with
-// bias, activation and residual between the scaling and the rounding.
+// What a warp carries from tile to tile: chunks done, and the place of the
+// chunk whose residual is loaded next (lane 0).
+struct EpiState {
+    uint32_t n = 0, issued = 0;
+    int tile = 0, chunk = 0;
+};
+
+// The fused epilogue of one warp's part of an output tile, A rows = channels
+// and bf16 Y by TMA: 32 channels x 32 tokens at a time through the warp's own
+// staging buffer, with no barrier between warps.
 //
-// A thread's 16x256b fragments are channels q 32 + 16 h + 8 e + lane / 4 of
-// tokens 8 r + 2 (lane % 4) + k: the two factors of a gated output (8 channels
-// apart) are its e = 0 and e = 1, and the product leaves 16 channels per warp,
-// one 64-channel box per chunk instead of two.
+// A thread's 16x256b fragments are channels 16 h + 8 x + lane / 4 of the warp's
+// 32 and tokens 8 r + 2 (lane % 4) + k: the two factors of a gated output (8
+// channels apart) are its x = 0 and x = 1.  stmatrix.trans turns them into rows
+// of tokens, 64 bytes each (32 when gated), swizzled as the TMA store expects.
 //
-// The residual chunk comes by TMA into the staging buffer that the chunk of Y
-// leaves from, in the same swizzled layout: ldmatrix.trans gives a thread the
-// elements that its stmatrix.trans then overwrites, so nothing else is staged
-// and Y may be the residual.  While a chunk is worked on, the residuals of the
-// next kBufs - 1 chunks (of the next tile after the last) land in the other
-// buffers.
+// The residual chunk comes by TMA into the same buffer in the same layout:
+// ldmatrix.trans gives a thread the elements that its stmatrix.trans then
+// overwrites, so nothing else is staged and Y may be the residual.  The next
+// chunk's residual is on its way as soon as the store has read the buffer: the
+// first of a tile's during the MMAs.
 //
-// One barrier per chunk: before it, the issuing thread has seen the store that
-// read the next chunk's buffer finish, so past it every warp may write there.
-//
-// kBatch chunks are read from tensor memory together: two where there is one
-// accumulator and a group has four chunks, which is then released after one
-// step of the loop (all four do not fit in registers beside the epilogue's).
-//
-// n: chunks this group has processed; issued: residual loads issued (issuer).
 // tile_at(i): the i-th tile of this cluster (>= n_tiles: none); release gives
-// the accumulator back (one lane).  Returns false when a bounded wait ran out
-// (all four warps alike).
-template <typename C, int kQ, int kBufs, int kBatch, typename TileAt, typename Release>
+// the accumulator back (one lane).  Returns false when a bounded wait ran out.
+template <int kQ, typename TileAt, typename Release>
 __device__ __forceinline__ bool epi_tile_channels(
-    const GemmArgs& args, const EpiWalk& walk, const CUtensorMap& tm_y, const CUtensorMap& tm_r,
-    uint8_t* stage, uint64_t* res_full, volatile int* abort_flag, uint32_t& n, uint32_t& issued,
-    int n_tiles, int a_cta0, int b0, uint32_t grp_bar, int q, int lane, bool issuer,
-    uint32_t t_row, TileAt tile_at, Release release) {
+    const GemmArgs& args, const EpiWalk& walk, EpiState& st, const CUtensorMap& tm_y,
+    const CUtensorMap& tm_r, uint8_t* buf, uint64_t* res_full, volatile int* abort_flag,
+    int n_tiles, int a_warp0, int b0, int lane, uint32_t t_row, TileAt tile_at, Release release) {
     constexpr bool kInt8 = kQ == kQInt8;
-    static_assert(kBufs == 2 || kBufs == 4, "staging buffers");
     const EpiArgs& e = args.epi;
     const int t4 = lane >> 2, tm = lane & 3;
-    const int mi = lane >> 3, mj = lane & 7;  // this thread's stmatrix matrix / row
-    // residual load of this group's chunk number j into buffer j % kBufs
-    auto load_residual = [&](uint32_t j) {
-        const int tile = tile_at(static_cast<int>(j / walk.per_tile));
+    const uint32_t sy = smem_u32(buf);
+    auto load_residual = [&] {  // lane 0: the warp's next residual chunk
+        const int tile = tile_at(st.tile);
         if (tile >= n_tiles) return;
         int ta, tb;
         tile_coords(tile, walk.nA, walk.nB, args.a_groups, ta, tb);
-        const int ch = ta * walk.tile_a_rows + a_cta0 % walk.tile_a_rows;
-        const int tok = tb * walk.tile_b_rows + walk.tok_off + walk.first +
-                        walk.step * static_cast<int>(j % walk.per_tile);
-        uint8_t* dst = stage + (j % kBufs) * C::kEpiBytes;
-        mbar_arrive_expect_tx(&res_full[j % kBufs], C::kEpiBytes);
-        tma_load_2d(dst, &tm_r, &res_full[j % kBufs], ch, tok);
-        tma_load_2d(dst + 32 * 128, &tm_r, &res_full[j % kBufs], ch + 64, tok);
-        issued = j + 1;
+        mbar_arrive_expect_tx(res_full, kFusedWarpBytes);
+        tma_load_2d(buf, &tm_r, res_full, ta * walk.tile_a_rows + a_warp0 % walk.tile_a_rows,
+                    tb * walk.tile_b_rows + walk.tok_off + walk.first + walk.step * st.chunk);
+        ++st.issued;
+        if (++st.chunk == walk.per_tile) {
+            st.chunk = 0;
+            ++st.tile;
+        }
     };
-    // loads in flight ahead of the chunk worked on; with four buffers the one
-    // whose store was issued last is left alone
-    constexpr int kAhead = kBufs == 2 ? 1 : kBufs - 2;
-    if (args.tma_res && issuer && n == 0)
-        for (int j = 0; j < kAhead; ++j) load_residual(j);
+    if (args.tma_res && st.issued == 0 && lane == 0) load_residual();
+    // blocks of this thread's stmatrix rows: matrix mi, row mj.  Row = token;
+    // its 16-byte unit of 8 channels is swizzled by the token as SWIZZLE_64B
+    // (32B when gated) does.
+    const int mi = lane >> 3, mj = lane & 7;
     float sa2[2][2], bias2[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int ch = a_cta0 + q * 32 + 16 * h + t4 + 8 * x;
+            const int ch = a_warp0 + 16 * h + t4 + 8 * x;
             sa2[h][x] = kQ == kQNvfp4 ? __ldg(args.s_a)
                                       : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
             bias2[h][x] = epi_bias(e, ch, ch < args.rowsA);
         }
 #pragma unroll 1
-    for (int cb = 0; cb < walk.per_tile; cb += kBatch) {
-        uint32_t v[kBatch][2][16];
-#pragma unroll
-        for (int cc = 0; cc < kBatch; ++cc) {
-            const int c = walk.first + walk.step * (cb + cc);
-            if (cb + cc < walk.per_tile) {
-                tmem_ld_16x256b_x4(t_row + c, v[cc][0]);
-                tmem_ld_16x256b_x4(t_row + (16u << 16) + c, v[cc][1]);
-            }
-        }
-        // the token scales of the first chunk arrive while tensor memory is read
+    for (int j = 0; j < walk.per_tile; ++j) {
+        const int c = walk.first + walk.step * j;
+        uint32_t v[32];  // [16 h + 4 r + 2 x + k]
+        tmem_ld_16x256b_x4(t_row + c, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
+        tmem_ld_16x256b_x4(t_row + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
+        // the token scales arrive while tensor memory is read
         float sb[4][2];
-        auto load_sb = [&](int c) {
+        const int tok = b0 + c + 2 * tm;
+        if (kQ != kQNvfp4 && kQ != kQBf16 && b0 + c + 32 <= args.rowsB) {
+            const float2* p = reinterpret_cast<const float2*>(args.s_b + tok);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const int tok = b0 + c + 8 * r + 2 * tm;
-                if (kQ != kQNvfp4 && kQ != kQBf16 && tok + 1 < args.rowsB) {
-                    const float2 s = __ldg(reinterpret_cast<const float2*>(args.s_b + tok));
-                    sb[r][0] = s.x;
-                    sb[r][1] = s.y;
-                } else {
-                    sb[r][0] = load_b_scale<kQ>(args.s_b, tok, tok < args.rowsB);
-                    sb[r][1] = load_b_scale<kQ>(args.s_b, tok + 1, tok + 1 < args.rowsB);
-                }
+                const float2 s = __ldg(p + 4 * r);
+                sb[r][0] = s.x;
+                sb[r][1] = s.y;
             }
-        };
-        load_sb(walk.first + walk.step * cb);
+        } else {
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    sb[r][k] = load_b_scale<kQ>(args.s_b, tok + 8 * r + k,
+                                                tok + 8 * r + k < args.rowsB);
+        }
         tmem_ld_wait();
-        if (cb + kBatch >= walk.per_tile) {  // last read: release
+        if (j + 1 == walk.per_tile) {  // last read: release
             tc_fence_before();
             __syncwarp();
             if (lane == 0) release();
         }
+        float y[32];
 #pragma unroll
-        for (int cc = 0; cc < kBatch; ++cc) {
-            if (cb + cc >= walk.per_tile) break;
-            const int c = walk.first + walk.step * (cb + cc);
-            if (cc > 0) load_sb(c);
-            uint8_t* buf = stage + (n % kBufs) * C::kEpiBytes;
-            const uint32_t sy = smem_u32(buf);
-            if (args.tma_res && issuer) {
-                bulk_wait_read<kBufs == 2 ? 0 : 1>();
-                load_residual(n + kAhead);
-            }
-            float y[32];  // [16 h + 4 r + 2 x + k]
+        for (int i = 0; i < 32; i += 2) {
+            const float x0 = kInt8 ? __int2float_rn(static_cast<int32_t>(v[i]))
+                                   : __uint_as_float(v[i]);
+            const float x1 = kInt8 ? __int2float_rn(static_cast<int32_t>(v[i + 1]))
+                                   : __uint_as_float(v[i + 1]);
+            const int h = i >> 4, r = (i >> 2) & 3, x = (i >> 1) & 1;
+            mul_rn_f32x2(x0, x1, sb[r][0], sb[r][1], y[i], y[i + 1]);
+            fma_rn_f32x2(y[i], y[i + 1], sa2[h][x], sa2[h][x], bias2[h][x], bias2[h][x], y[i],
+                         y[i + 1]);
+        }
+        if (e.gated) {
+            activate<true>(y, e.act);
+            uint32_t pk[2][4];
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int j = 0; j < 16; j += 2) {
-                    const uint32_t b0_ = v[cc][h][j], b1_ = v[cc][h][j + 1];
-                    const float x0 = kInt8 ? __int2float_rn(static_cast<int32_t>(b0_))
-                                           : __uint_as_float(b0_);
-                    const float x1 = kInt8 ? __int2float_rn(static_cast<int32_t>(b1_))
-                                           : __uint_as_float(b1_);
-                    const int x = (j >> 1) & 1;
-                    float &y0 = y[16 * h + j], &y1 = y[16 * h + j + 1];
-                    mul_rn_f32x2(x0, x1, sb[j >> 2][0], sb[j >> 2][1], y0, y1);
-                    fma_rn_f32x2(y0, y1, sa2[h][x], sa2[h][x], bias2[h][x], bias2[h][x], y0, y1);
+                for (int r = 0; r < 4; ++r) {
+                    const int i = 16 * h + 4 * r;
+                    float y0, y1;
+                    mul_rn_f32x2(y[i], y[i + 1], y[i + 2], y[i + 3], y0, y1);
+                    pk[h][r] = pack_bf16(y0, y1);
                 }
-            bool got = true;
-            if (e.gated) {
-                activate<true>(y, e.act);
-                uint32_t pk[2][4];
+            if (lane == 0) bulk_wait_read<0>();  // the last store has read the buffer
+            __syncwarp();
+            const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3 of channel block h
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int i = 16 * h + 4 * r;
-                        float y0, y1;
-                        mul_rn_f32x2(y[i], y[i + 1], y[i + 2], y[i + 3], y0, y1);
-                        pk[h][r] = pack_bf16(y0, y1);
-                    }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3
-                    stmatrix_x4_trans(sy + tok * 128 + (((2 * q + h) ^ (tok & 7)) << 4), pk[h][0],
-                                      pk[h][1], pk[h][2], pk[h][3]);
-                }
-            } else {
-                activate<false>(y, e.act);
-                if (args.tma_res) {
-                    got = mbar_wait(&res_full[n % kBufs], (n / kBufs) & 1, abort_flag);
-                    __syncwarp();
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int rp = 0; rp < 2; ++rp) {
-                            uint32_t rr[4];
-                            ldmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj), rr);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const int i = 16 * h + 8 * rp + 2 * j;
-                                add_rn_f32x2(y[i], y[i + 1], __uint_as_float(rr[j] << 16),
-                                             __uint_as_float(rr[j] & 0xFFFF0000u), y[i], y[i + 1]);
-                            }
-                        }
-                }
+            for (int h = 0; h < 2; ++h)
+                stmatrix_x4_trans(sy + tok * 32 + ((h ^ ((tok >> 2) & 1)) << 4), pk[h][0],
+                                  pk[h][1], pk[h][2], pk[h][3]);
+        } else {
+            activate<false>(y, e.act);
+            // matrices of (h, rp): (r = 2 rp, x = 0), (2 rp, 1), (2 rp + 1, 0), (2 rp + 1, 1)
+            auto block = [&](int h, int rp) {
+                const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
+                return sy + tok * 64 + (((2 * h + (mi & 1)) ^ ((tok >> 1) & 3)) << 4);
+            };
+            if (args.tma_res) {
+                const bool got = mbar_wait(res_full, st.n & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) return false;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int rp = 0; rp < 2; ++rp) {
-                        const int i = 16 * h + 8 * rp;
-                        stmatrix_x4_trans(epi_block_addr(sy, rp, q, h, mi, mj),
-                                          pack_bf16(y[i], y[i + 1]), pack_bf16(y[i + 2], y[i + 3]),
-                                          pack_bf16(y[i + 4], y[i + 5]),
-                                          pack_bf16(y[i + 6], y[i + 7]));
+                        uint32_t rr[4];
+                        ldmatrix_x4_trans(block(h, rp), rr);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int i = 16 * h + 8 * rp + 2 * j;
+                            add_rn_f32x2(y[i], y[i + 1], __uint_as_float(rr[j] << 16),
+                                         __uint_as_float(rr[j] & 0xFFFF0000u), y[i], y[i + 1]);
+                        }
                     }
+            } else {
+                if (lane == 0) bulk_wait_read<0>();
+                __syncwarp();
             }
-            fence_async_shared();
-            // the store that read the next chunk's buffer is done (n - 1 or n - 3)
-            if (issuer) bulk_wait_read<kBufs - 2>();
-            if (!named_bar_and(grp_bar, 128, got)) return false;
-            if (issuer) {
-                const uint64_t stream = l2_policy_evict_first();
-                if (e.gated) {
-                    tma_store_2d_hint(&tm_y, buf, a_cta0 / 2, b0 + c, stream);
-                } else {
-                    tma_store_2d_hint(&tm_y, buf, a_cta0, b0 + c, stream);
-                    tma_store_2d_hint(&tm_y, buf + 32 * 128, a_cta0 + 64, b0 + c, stream);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int rp = 0; rp < 2; ++rp) {
+                    const int i = 16 * h + 8 * rp;
+                    stmatrix_x4_trans(block(h, rp), pack_bf16(y[i], y[i + 1]),
+                                      pack_bf16(y[i + 2], y[i + 3]),
+                                      pack_bf16(y[i + 4], y[i + 5]),
+                                      pack_bf16(y[i + 6], y[i + 7]));
                 }
-                bulk_commit_group();
+        }
+        fence_async_shared();
+        __syncwarp();
+        ++st.n;
+        if (lane == 0) {
+            tma_store_2d_hint(&tm_y, buf, e.gated ? a_warp0 / 2 : a_warp0, b0 + c,
+                              l2_policy_evict_first());
+            bulk_commit_group();
+            if (args.tma_res) {
+                bulk_wait_read<0>();
+                load_residual();
             }
-            ++n;
         }
     }
     return true;
+}
+
+// After a wait that ran out: the residual load in flight lands (lane 0).
+__device__ __forceinline__ void epi_drain(const EpiState& st, uint64_t* res_full) {
+    if (st.n < st.issued) mbar_drain(res_full, st.n & 1);
 }
 
 // kQ: kQE4M3, kQInt8 (kind::f8f6f4 / kind::i8), kQBf16 (kind::f16) or kQNvfp4
@@ -522,7 +510,7 @@ __device__ __forceinline__ bool epi_tile_channels(
 // unused otherwise, and s_a is one global scale).  kEpi: the fused epilogue of
 // args.epi (ss_epilogue.cuh; tm_r is the residual's map, shaped as Y's).
 template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi = false>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_e, const __grid_constant__ CUtensorMap tm_y,
                 const __grid_constant__ CUtensorMap tm_sfa,
@@ -531,6 +519,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     constexpr bool kInt8 = kQ == kQInt8;
     constexpr bool kBf16 = kQ == kQBf16;
     constexpr bool kFp4 = kQ == kQNvfp4;
+    constexpr int kEpiWarps = kEpi ? kFusedEpiWarps : kGemmEpiWarps;
+    constexpr int kGroups = kEpiWarps / 4;  // of four epilogue warps
     using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi>,
                                  GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi>>;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
@@ -541,8 +531,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     uint64_t* acc_full = empty + C::kStages;  // [2]: one per accumulator buffer
     uint64_t* acc_empty = acc_full + 2;
     uint64_t* drain = acc_empty + 2;
-    uint64_t* res_full = drain + 1;  // [2 groups][2 buffers]: a chunk's residual has landed (kEpi)
-    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(res_full + 4);
+    uint64_t* res_full = drain + 1;  // per epilogue warp: its residual chunk has landed (kEpi)
+    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(res_full + (kEpi ? kEpiWarps : 0));
     __shared__ int abort_flag_storage;
     volatile int* abort_flag = &abort_flag_storage;
     pdl_trigger();
@@ -568,10 +558,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&acc_full[b], 1);
-            mbar_init(&acc_empty[b], kGemmEpiWarps * kPair);
+            mbar_init(&acc_empty[b], kEpiWarps * kPair);
         }
         mbar_init(drain, 1);
-        for (int b = 0; b < 4; ++b) mbar_init(&res_full[b], 1);
+        for (int b = 0; kEpi && b < kEpiWarps; ++b) mbar_init(&res_full[b], 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -861,10 +851,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         const bool issuer = (ew & 3) == 0 && lane == 0;
         const uint32_t acc_empty_leader = kPair == 2 ? map_to_rank(acc_empty, 0) : 0u;
         constexpr int kEsz = 2;  // TMA-store staging is used for bf16 output only
-        uint8_t* sy = smem + C::kEpiOffset + grp * (C::kEpiBufs / 2) * C::kEpiBytes;
+        uint8_t* sy = smem + C::kEpiOffset + grp * C::kEpiBytes;
         int i = 0;
         bool ok = true;
-        uint32_t epi_n = 0, epi_issued = 0;  // chunks processed, residual loads issued (kEpi)
+        [[maybe_unused]] EpiState epi;
         for (int t = unit; t < n_tiles && ok; t += n_units, ++i) {
             int ta, tb;
             tile_coords(t, nA, nB, args.a_groups, ta, tb);
@@ -874,8 +864,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t aph = C::kAccBufs == 2 ? ((i >> 1) & 1) : (i & 1);
             // the four warps of a group take the same decision, so none is
             // left behind at the group's named barrier if the wait gives up
+            // (the fused epilogue's warps share nothing and decide alone)
             const bool got = mbar_wait(&acc_full[acc], aph, abort_flag);
-            if (!named_bar_and(grp_bar, 128, got)) {
+            if (!(kEpi ? __all_sync(0xffffffffu, got) != 0 : named_bar_and(grp_bar, 128, got))) {
                 ok = false;
                 break;
             }
@@ -897,21 +888,20 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
             if constexpr (kEpi && kOutBf16) {
-                if (args.tma_store && args.a_is_w) {
-                    // as the path below, with the fused epilogue
-                    const EpiWalk walk = {32 * grp, 64,  (args.bn - 32 * grp + 63) / 64, 0,
-                                          args.bn,  tile_a_rows, nA, nB};
-                    if (!epi_tile_channels<C, kQ, C::kEpiBufs / 2, C::kAccBufs == 1 ? 2 : 1>(
-                            args, walk, tm_y, tm_r, sy, &res_full[2 * grp], abort_flag, epi_n,
-                            epi_issued, n_tiles, a_cta0, b0, grp_bar, q, lane, issuer, t_row,
-                            [&](int j) { return unit + j * n_units; },
-                            [&] {
-                                if constexpr (kPair == 2)
-                                    mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
-                                else
-                                    mbar_arrive(&acc_empty[acc]);
-                            }))
-                        ok = false;
+                if (args.tma_store) {  // (channel rows)
+                    const EpiWalk walk = {32 * grp, 32 * kGroups,
+                                          (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups),
+                                          0, args.bn, tile_a_rows, nA, nB};
+                    ok = epi_tile_channels<kQ>(
+                        args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
+                        &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row,
+                        [&](int j) { return unit + j * n_units; },
+                        [&] {
+                            if constexpr (kPair == 2)
+                                mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
+                            else
+                                mbar_arrive(&acc_empty[acc]);
+                        });
                     continue;
                 }
             }
@@ -1043,13 +1033,40 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
                 continue;
             }
-            for (int c = 32 * grp; c < args.bn; c += 64) {
+            for (int c = 32 * grp; c < args.bn; c += 32 * kGroups) {
                 const int bc = b0 + c + lane;  // this lane's B row of the chunk
                 const float sb_lane = load_b_scale<kQ>(args.s_b, bc, bc < args.rowsB);
+                if constexpr (kEpi) {
+                    const float bias_row = args.a_is_w ? epi_bias(args.epi, a_row, row_ok) : 0.0f;
+                    const float bias_col =
+                        args.a_is_w ? 0.0f : epi_bias(args.epi, bc, bc < args.rowsB);
+#pragma unroll 1
+                    for (int half = 0; half < 32; half += 16) {
+                        uint32_t r[16];
+                        tmem_ld_32x32b_x16(t_row + c + half, r);
+                        tmem_ld_wait();
+                        if (half == 16 && c + 32 * kGroups >= args.bn) {  // last read: release
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) {
+                                if constexpr (kPair == 2)
+                                    mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
+                                else
+                                    mbar_arrive(&acc_empty[acc]);
+                            }
+                        }
+                        const int from = (lane & 15) + half;
+                        epi_store_direct<kInt8, kOutBf16>(
+                            args, r, a_row, b0 + c + half, sa,
+                            __shfl_sync(0xffffffffu, sb_lane, from), bias_row,
+                            __shfl_sync(0xffffffffu, bias_col, from));
+                    }
+                    continue;
+                }
                 uint32_t r[32];
                 tmem_ld_32x32b_x32(t_row + c, r);
                 tmem_ld_wait();
-                if (c + 64 >= args.bn) {  // this group's last read: release its part
+                if (c + 32 * kGroups >= args.bn) {  // this group's last read: release its part
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) {
@@ -1059,9 +1076,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                             mbar_arrive(&acc_empty[acc]);
                     }
                 }
-                if constexpr (kEpi) {
-                    epi_store_direct<kInt8, kOutBf16>(args, r, a_row, b0 + c, lane, sa, sb_lane);
-                } else if (args.tma_store) {
+                if (args.tma_store) {
                     if (issuer) bulk_wait_read<0>();  // the group's last store has read it
                     named_bar_sync(grp_bar, 128);
                     if (args.a_is_w) {
@@ -1127,9 +1142,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
                 }
             }
         }
-        if constexpr (kEpi) {  // after a wait that ran out: residual loads in flight land
-            for (; issuer && epi_n < epi_issued; ++epi_n)
-                mbar_drain(&res_full[2 * grp + (epi_n & 1)], (epi_n >> 1) & 1);
+        if (kEpi && lane == 0) {
+            epi_drain(epi, &res_full[ew]);
+            bulk_wait_all();  // Y stores done reading shared memory
         }
         if (issuer) bulk_wait_all();  // Y stores done reading shared memory
     }

@@ -59,10 +59,9 @@ struct WideCfg {
     static constexpr int kEOffset = kBOffset + kWideBT * kBTileBytes;
     static constexpr int kStageBytes = (kEOffset + kEBytes + 1023) / 1024 * 1024;
     static constexpr int kEpiBytes = 32 * kTileA * 2;     // one [32 tokens][128 channels] chunk
-    // Y chunks staged per B tile: two, or with the fused epilogue four, so that
-    // two residual chunks are on their way while one is worked on
-    static constexpr int kEpiBufs = kEpi ? 4 : 2;
-    static constexpr int kEpiGroupBytes = kEpiBufs * kEpiBytes;
+    static constexpr int kEpiGroupBytes = 2 * kEpiBytes;  // double buffer per B tile
+    static constexpr int kEpiWarps = kEpi ? kFusedEpiWarps : 8;
+    static_assert(!kEpi || kWideBT * kEpiGroupBytes == kEpiWarps * kFusedWarpBytes, "staging");
     static constexpr int kBarBytes = 256;
     static constexpr int kStages =
         (227 * 1024 - 1024 - kBarBytes - 64 - kWideBT * kBnMax * 4 - kWideBT * kEpiGroupBytes) /
@@ -75,6 +74,7 @@ struct WideCfg {
     static constexpr int kAccStride = kBnMax;             // TMEM columns per accumulator
     static constexpr int kECol = kWideBT * kBnMax;        // metadata: 4 columns per stage
     static_assert(kECol + 4 * kStages <= kTmemCols, "TMEM budget");
+    static_assert((2 * kStages + 3 + (kEpi ? kEpiWarps : 0)) * 8 + 4 <= kBarBytes, "barrier area");
     static_assert(kStages >= 4, "pipeline depth");
     static_assert(kSmemBytes + 1024 <= 227 * 1024, "shared memory budget (with static)");
     static_assert(kBOffset % 1024 == 0 && kBTileBytes % 1024 == 0 && kEOffset % 16 == 0,
@@ -91,11 +91,11 @@ __device__ __forceinline__ int snake_tile(int k, int unit, int n_units) {
 // kAIsW: A rows are output channels (weight-sparse, Y[b, a]); otherwise A
 // rows are tokens (activation-sparse, Y[a, b]).
 // kEpi (kAIsW only): the fused epilogue of args.epi (ss_epilogue.cuh; tm_r is
-// the residual's map).  A group then takes its accumulator chunk by chunk
+// the residual's map).  Sixteen warps then take an accumulator chunk by chunk
 // (epi_tile_channels) instead of holding it as packed bf16: what the bias, the
 // activation and the residual are added to is not rounded yet.
 template <bool kInt8, bool kAIsW, bool kEpi = false>
-__global__ void __launch_bounds__(kWideThreads, 1)
+__global__ void __launch_bounds__(kEpi ? kFusedThreads : kWideThreads, 1)
     gemm_sparse_wide_kernel(const __grid_constant__ CUtensorMap tm_a,
                             const __grid_constant__ CUtensorMap tm_b,
                             const __grid_constant__ CUtensorMap tm_e,
@@ -111,9 +111,8 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     uint64_t* acc_full = empty + C::kStages;
     uint64_t* acc_empty = acc_full + 1;
     uint64_t* drain = acc_empty + 1;
-    uint64_t* res_full = drain + 1;  // [2 B tiles][kEpiBufs]: a residual chunk has landed (kEpi)
-    uint32_t* tmem_base_slot =
-        reinterpret_cast<uint32_t*>(res_full + (kEpi ? kWideBT * C::kEpiBufs : 0));
+    uint64_t* res_full = drain + 1;  // per epilogue warp: its residual chunk has landed (kEpi)
+    uint32_t* tmem_base_slot = reinterpret_cast<uint32_t*>(res_full + (kEpi ? C::kEpiWarps : 0));
     __shared__ int abort_flag_storage;
     volatile int* abort_flag = &abort_flag_storage;
     pdl_trigger();
@@ -138,9 +137,9 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             mbar_init(&empty[s], 1);
         }
         mbar_init(acc_full, 1);
-        mbar_init(acc_empty, 8 * 2);  // 8 epilogue warps in each CTA of the pair
+        mbar_init(acc_empty, C::kEpiWarps * 2);  // the epilogue warps of both CTAs of the pair
         mbar_init(drain, 1);
-        for (int b = 0; kEpi && b < kWideBT * C::kEpiBufs; ++b) mbar_init(&res_full[b], 1);
+        for (int b = 0; kEpi && b < C::kEpiWarps; ++b) mbar_init(&res_full[b], 1);
         fence_barrier_init();
     }
     if (warp == 1) {
@@ -314,7 +313,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int ew = warp - 2;
         const int et = ew * 32 + lane;  // 0..255
         const int q = warp & 3;  // TMEM lane quarter this warp may access
-        const int bt = ew >> 2;  // B tile (accumulator) of this warp
+        const int bt = kEpi ? ew >> 3 : ew >> 2;  // B tile (accumulator) of this warp
         const bool issuer = (ew & 3) == 0 && lane == 0;
         const uint32_t grp_bar = 2 + static_cast<uint32_t>(bt);
         const uint32_t acc_empty_leader = map_to_rank(acc_empty, 0);
@@ -324,7 +323,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
         const int mi = lane >> 3, mj = lane & 7;  // this thread's stmatrix matrix / row
         int i = 0;
         uint32_t chunk_iter = 0;
-        [[maybe_unused]] uint32_t epi_n = 0, epi_issued = 0;
+        [[maybe_unused]] EpiState epi;
         for (int t = snake_tile(0, unit, n_units); t < n_tiles;
              ++i, t = snake_tile(i, unit, n_units)) {
             int ta, tb_;
@@ -334,20 +333,20 @@ __global__ void __launch_bounds__(kWideThreads, 1)
             const int tok0 = tile_tok0 + bt * args.bn;
             if constexpr (kEpi) {
                 const bool ready = mbar_wait(acc_full, static_cast<uint32_t>(i & 1), abort_flag);
-                if (!named_bar_and(grp_bar, 128, ready)) break;
+                if (!__all_sync(0xffffffffu, ready)) break;
                 tc_fence_after();
-                const EpiWalk walk = {0, 32, args.bn / 32, bt * args.bn, tile_b_rows, kPairRows,
-                                      nA, nB};
-                const bool done = epi_tile_channels<C, kInt8 ? kQInt8 : kQE4M3, C::kEpiBufs, 1>(
-                    args, walk, tm_y, tm_r, stage_y, &res_full[C::kEpiBufs * bt], abort_flag,
-                    epi_n, epi_issued, n_tiles, a_cta0, tok0, grp_bar, q, lane, issuer,
+                const int first = 32 * ((ew >> 2) & 1);  // two groups per B tile
+                const EpiWalk walk = {first, 64, (args.bn - first + 63) / 64, bt * args.bn,
+                                      tile_b_rows, kPairRows, nA, nB};
+                const bool done = epi_tile_channels<kInt8 ? kQInt8 : kQE4M3>(
+                    args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
+                    &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, tok0, lane,
                     tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                         static_cast<uint32_t>(bt * C::kAccStride),
                     [&](int j) { return snake_tile(j, unit, n_units); },
                     [&] { mbar_arrive_cluster(acc_empty_leader); });
                 if (!done) break;
-                continue;
-            }
+            } else {
             // scales of this tile, fetched while its MMAs still run
             float sb_pre[2];
 #pragma unroll
@@ -504,11 +503,11 @@ __global__ void __launch_bounds__(kWideThreads, 1)
                     ++chunk_iter;
                 }
             }
+            }  // !kEpi
         }
-        if constexpr (kEpi) {  // after a wait that ran out: residual loads in flight land
-            for (; issuer && epi_n < epi_issued; ++epi_n)
-                mbar_drain(&res_full[C::kEpiBufs * bt + epi_n % C::kEpiBufs],
-                           (epi_n / C::kEpiBufs) & 1);
+        if (kEpi && lane == 0) {
+            epi_drain(epi, &res_full[ew]);
+            bulk_wait_all();
         }
         if (issuer) bulk_wait_all();  // Y stores done reading shared memory
     }
