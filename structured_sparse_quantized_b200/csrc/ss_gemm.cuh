@@ -374,26 +374,36 @@ __device__ __forceinline__ bool epi_tile_channels(
     // its 16-byte unit of 8 channels is swizzled by the token as SWIZZLE_64B
     // (32B when gated) does.
     const int mi = lane >> 3, mj = lane & 7;
+    // matrices of (h, rp): (r = 2 rp, x = 0), (2 rp, 1), (2 rp + 1, 0), (2 rp + 1, 1)
+    auto block = [&](int h, int rp) {
+        const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
+        return sy + tok * 64 + (((2 * h + (mi & 1)) ^ ((tok >> 1) & 3)) << 4);
+    };
+    // scales of the fragment's channels (one for the whole tensor in NVFP4) and bias
+    constexpr bool kFp4 = kQ == kQNvfp4;
     float sa2[2][2], bias2[2][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             const int ch = a_warp0 + 16 * h + t4 + 8 * x;
-            sa2[h][x] = kQ == kQNvfp4 ? __ldg(args.s_a)
-                                      : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
+            sa2[h][x] = kFp4 ? __ldg(args.s_a)
+                             : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
             bias2[h][x] = epi_bias(e, ch, ch < args.rowsA);
         }
-#pragma unroll 1
-    for (int j = 0; j < walk.per_tile; ++j) {
-        const int c = walk.first + walk.step * j;
-        uint32_t v[32];  // [16 h + 4 r + 2 x + k]
+    auto read = [&](int c, uint32_t (&v)[32]) {  // [16 h + 4 r + 2 x + k]
         tmem_ld_16x256b_x4(t_row + c, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
         tmem_ld_16x256b_x4(t_row + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
-        // the token scales arrive while tensor memory is read
+    };
+    // One chunk: the accumulator v at column c to its packed result, in the
+    // order of the staged 8x8 blocks (gated: the first half).
+    auto compute = [&](int c, const uint32_t (&v)[32], uint32_t (&pk)[16]) {
         float sb[4][2];
         const int tok = b0 + c + 2 * tm;
-        if (kQ != kQNvfp4 && kQ != kQBf16 && b0 + c + 32 <= args.rowsB) {
+        if (kFp4 || kQ == kQBf16) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sb[r][0] = sb[r][1] = kFp4 ? __ldg(args.s_b) : 1.0f;
+        } else if (b0 + c + 32 <= args.rowsB) {
             const float2* p = reinterpret_cast<const float2*>(args.s_b + tok);
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
@@ -406,14 +416,7 @@ __device__ __forceinline__ bool epi_tile_channels(
             for (int r = 0; r < 4; ++r)
 #pragma unroll
                 for (int k = 0; k < 2; ++k)
-                    sb[r][k] = load_b_scale<kQ>(args.s_b, tok + 8 * r + k,
-                                                tok + 8 * r + k < args.rowsB);
-        }
-        tmem_ld_wait();
-        if (j + 1 == walk.per_tile) {  // last read: release
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) release();
+                    sb[r][k] = tok + 8 * r + k < args.rowsB ? __ldg(args.s_b + tok + 8 * r + k) : 0.0f;
         }
         float y[32];
 #pragma unroll
@@ -429,60 +432,49 @@ __device__ __forceinline__ bool epi_tile_channels(
         }
         if (e.gated) {
             activate<true>(y, e.act);
-            uint32_t pk[2][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 32; i += 4) {
+                float y0, y1;
+                mul_rn_f32x2(y[i], y[i + 1], y[i + 2], y[i + 3], y0, y1);
+                pk[i >> 2] = pack_bf16(y0, y1);
+            }
+            return true;
+        }
+        activate<false>(y, e.act);
+        if (args.tma_res) {
+            const bool got = mbar_wait(res_full, st.n & 1, abort_flag);
+            if (!__all_sync(0xffffffffu, got)) return false;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int i = 16 * h + 4 * r;
-                    float y0, y1;
-                    mul_rn_f32x2(y[i], y[i + 1], y[i + 2], y[i + 3], y0, y1);
-                    pk[h][r] = pack_bf16(y0, y1);
-                }
+            for (int i = 0; i < 32; i += 8) {
+                uint32_t rr[4];
+                ldmatrix_x4_trans(block(i >> 4, (i >> 3) & 1), rr);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    add_rn_f32x2(y[i + 2 * k], y[i + 2 * k + 1], __uint_as_float(rr[k] << 16),
+                                 __uint_as_float(rr[k] & 0xFFFF0000u), y[i + 2 * k],
+                                 y[i + 2 * k + 1]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) pk[i >> 1] = pack_bf16(y[i], y[i + 1]);
+        return true;
+    };
+    auto store = [&](int c, const uint32_t (&pk)[16]) {
+        if (!args.tma_res) {  // (with a residual, its load waited for this already)
             if (lane == 0) bulk_wait_read<0>();  // the last store has read the buffer
             __syncwarp();
+        }
+        if (e.gated) {
             const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3 of channel block h
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                stmatrix_x4_trans(sy + tok * 32 + ((h ^ ((tok >> 2) & 1)) << 4), pk[h][0],
-                                  pk[h][1], pk[h][2], pk[h][3]);
+                stmatrix_x4_trans(sy + tok * 32 + ((h ^ ((tok >> 2) & 1)) << 4), pk[4 * h],
+                                  pk[4 * h + 1], pk[4 * h + 2], pk[4 * h + 3]);
         } else {
-            activate<false>(y, e.act);
-            // matrices of (h, rp): (r = 2 rp, x = 0), (2 rp, 1), (2 rp + 1, 0), (2 rp + 1, 1)
-            auto block = [&](int h, int rp) {
-                const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
-                return sy + tok * 64 + (((2 * h + (mi & 1)) ^ ((tok >> 1) & 3)) << 4);
-            };
-            if (args.tma_res) {
-                const bool got = mbar_wait(res_full, st.n & 1, abort_flag);
-                if (!__all_sync(0xffffffffu, got)) return false;
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-#pragma unroll
-                    for (int rp = 0; rp < 2; ++rp) {
-                        uint32_t rr[4];
-                        ldmatrix_x4_trans(block(h, rp), rr);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int i = 16 * h + 8 * rp + 2 * j;
-                            add_rn_f32x2(y[i], y[i + 1], __uint_as_float(rr[j] << 16),
-                                         __uint_as_float(rr[j] & 0xFFFF0000u), y[i], y[i + 1]);
-                        }
-                    }
-            } else {
-                if (lane == 0) bulk_wait_read<0>();
-                __syncwarp();
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int rp = 0; rp < 2; ++rp) {
-                    const int i = 16 * h + 8 * rp;
-                    stmatrix_x4_trans(block(h, rp), pack_bf16(y[i], y[i + 1]),
-                                      pack_bf16(y[i + 2], y[i + 3]),
-                                      pack_bf16(y[i + 4], y[i + 5]),
-                                      pack_bf16(y[i + 6], y[i + 7]));
-                }
+            for (int i = 0; i < 16; i += 4)
+                stmatrix_x4_trans(block(i >> 3, (i >> 2) & 1), pk[i], pk[i + 1], pk[i + 2],
+                                  pk[i + 3]);
         }
         fence_async_shared();
         __syncwarp();
@@ -495,6 +487,39 @@ __device__ __forceinline__ bool epi_tile_channels(
                 bulk_wait_read<0>();
                 load_residual();
             }
+        }
+    };
+    auto release_now = [&] {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) release();
+    };
+    const int c0 = walk.first, n_chunks = walk.per_tile;
+    if constexpr (kFp4) {
+        // One accumulator and at most two chunks per warp (256 columns, four
+        // groups): both are read and the accumulator released before any
+        // arithmetic, so that the next tile's MMAs start.
+        uint32_t v0[32], v1[32], pk[16];
+        read(c0, v0);
+        if (n_chunks > 1) read(c0 + walk.step, v1);
+        tmem_ld_wait();
+        release_now();
+        if (!compute(c0, v0, pk)) return false;
+        store(c0, pk);
+        if (n_chunks > 1) {
+            if (!compute(c0 + walk.step, v1, pk)) return false;
+            store(c0 + walk.step, pk);
+        }
+    } else {
+#pragma unroll 1
+        for (int j = 0; j < n_chunks; ++j) {
+            const int c = c0 + walk.step * j;
+            uint32_t v[32], pk[16];
+            read(c, v);
+            tmem_ld_wait();
+            if (j + 1 == n_chunks) release_now();
+            if (!compute(c, v, pk)) return false;
+            store(c, pk);
         }
     }
     return true;
