@@ -162,13 +162,13 @@ bool make_y_map(CUtensorMap* map, void* Y, int64_t M, int64_t N, bool out_bf16, 
                   : make_map_2d(map, Y, M, N, ss::kTileA, 32, CU_TENSOR_MAP_SWIZZLE_NONE, dt, esz);
 }
 
-template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi>
+template <bool kSparse, int kQ, bool kOutBf16, int kPair, int kEpi>
 ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& e,
                       const CUtensorMap& y, const CUtensorMap& r, const ss::GemmArgs& args,
                       cudaStream_t stream, const CUtensorMap* sfa = nullptr,
                       const CUtensorMap* sfb = nullptr) {
-    using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair, kEpi>,
-                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi>>;
+    using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair, kEpi != 0>,
+                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi != 0>>;
     auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
@@ -187,38 +187,48 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
                      e, y, sfa ? *sfa : a, sfb ? *sfb : a, r, args);
 }
 
-// q: ss::kQE4M3, kQInt8 or kQBf16; bf16: Y element type.
-template <bool kSparse, int kPair, bool kEpi>
-ss_status dispatch_gemm(int dev, int q, bool bf16, const CUtensorMap& a, const CUtensorMap& b,
-                        const CUtensorMap& e, const CUtensorMap& y, const CUtensorMap& r,
-                        const ss::GemmArgs& args, cudaStream_t st) {
+// The kernel for a Y type and, with a fused epilogue, its way (epilogue_maps).
+template <bool kSparse, int kQ, int kPair>
+ss_status dispatch_epi(int dev, bool bf16, bool fused, const CUtensorMap& a, const CUtensorMap& b,
+                       const CUtensorMap& e, const CUtensorMap& y, const CUtensorMap& r,
+                       const ss::GemmArgs& args, cudaStream_t st, const CUtensorMap* sfa = nullptr,
+                       const CUtensorMap* sfb = nullptr) {
     using namespace ss;
-    if (q == kQInt8)
-        return bf16 ? launch_gemm<kSparse, kQInt8, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
-                    : launch_gemm<kSparse, kQInt8, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
-    if (q == kQBf16)
-        return bf16 ? launch_gemm<kSparse, kQBf16, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
-                    : launch_gemm<kSparse, kQBf16, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
-    return bf16 ? launch_gemm<kSparse, kQE4M3, true, kPair, kEpi>(dev, a, b, e, y, r, args, st)
-                : launch_gemm<kSparse, kQE4M3, false, kPair, kEpi>(dev, a, b, e, y, r, args, st);
+#define SS_GEMM_GO(BF, E) \
+    return launch_gemm<kSparse, kQ, BF, kPair, E>(dev, a, b, e, y, r, args, st, sfa, sfb)
+    if (!fused) {
+        if (bf16) SS_GEMM_GO(true, kEpiNone);
+        SS_GEMM_GO(false, kEpiNone);
+    }
+    if (args.tma_store) {
+        if constexpr (kSparse && kQ != kQNvfp4)  // a sparse activation as A: token rows
+            if (!args.a_is_w) SS_GEMM_GO(true, kEpiTokens);
+        SS_GEMM_GO(true, kEpiChannels);
+    }
+    if (bf16) SS_GEMM_GO(true, kEpiDirect);
+    SS_GEMM_GO(false, kEpiDirect);
+#undef SS_GEMM_GO
 }
 
+// q: ss::kQE4M3, kQInt8 or kQBf16; bf16: Y element type.
 template <bool kSparse>
-ss_status dispatch_gemm_any(int dev, int q, bool bf16, int pair, bool fused, const CUtensorMap& a,
-                            const CUtensorMap& b, const CUtensorMap& e, const CUtensorMap& y,
-                            const CUtensorMap& r, const ss::GemmArgs& args, cudaStream_t st) {
-    if (pair == 1)
-        return fused ? dispatch_gemm<kSparse, 1, true>(dev, q, bf16, a, b, e, y, r, args, st)
-                     : dispatch_gemm<kSparse, 1, false>(dev, q, bf16, a, b, e, y, r, args, st);
-    return fused ? dispatch_gemm<kSparse, 2, true>(dev, q, bf16, a, b, e, y, r, args, st)
-                 : dispatch_gemm<kSparse, 2, false>(dev, q, bf16, a, b, e, y, r, args, st);
+ss_status dispatch_gemm(int dev, int q, bool bf16, int pair, bool fused, const CUtensorMap& a,
+                        const CUtensorMap& b, const CUtensorMap& e, const CUtensorMap& y,
+                        const CUtensorMap& r, const ss::GemmArgs& args, cudaStream_t st) {
+    using namespace ss;
+#define SS_GEMM_Q(Q)                                                                          \
+    return pair == 1 ? dispatch_epi<kSparse, Q, 1>(dev, bf16, fused, a, b, e, y, r, args, st) \
+                     : dispatch_epi<kSparse, Q, 2>(dev, bf16, fused, a, b, e, y, r, args, st)
+    if (q == kQInt8) SS_GEMM_Q(kQInt8);
+    if (q == kQBf16) SS_GEMM_Q(kQBf16);
+    SS_GEMM_Q(kQE4M3);
+#undef SS_GEMM_Q
 }
 
 // Maps and paths of Y and the residual (N columns of Y; A rows = channels or
 // not): sets args.tma_store and args.tma_res; unused maps are copies of `any`.
-// A fused epilogue takes the TMA path for bf16 Y and channel rows, unless the
-// residual is fp32; its warps store boxes of 32 tokens x 32 channels (16 of a
-// gated product).
+// A fused epilogue takes the TMA path for bf16 Y, unless the residual is fp32;
+// its warps store boxes of 32 tokens x 32 channels (16 of a gated product).
 void epilogue_maps(const CUtensorMap& any, void* Y, int64_t M, int64_t N, bool bf16, bool fused,
                    ss::GemmArgs* args, CUtensorMap* y, CUtensorMap* r) {
     *y = *r = any;
@@ -233,8 +243,7 @@ void epilogue_maps(const CUtensorMap& any, void* Y, int64_t M, int64_t N, bool b
                            gated ? CU_TENSOR_MAP_SWIZZLE_32B : CU_TENSOR_MAP_SWIZZLE_64B,
                            CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
     };
-    args->tma_store =
-        bf16 && args->a_is_w && N % 8 == 0 && !args->epi.res_f32 && box(y, Y) ? 1 : 0;
+    args->tma_store = bf16 && N % 8 == 0 && !args->epi.res_f32 && box(y, Y) ? 1 : 0;
     if (args->tma_store && args->epi.residual) {
         args->tma_res = box(r, args->epi.residual) ? 1 : 0;
         args->tma_store = args->tma_res;
@@ -447,10 +456,29 @@ bool prefer_wide(int64_t rowsA, int64_t rowsB, int bn_narrow, int units) {
     return 1.8 * static_cast<double>(waves_w) < static_cast<double>(waves_n);
 }
 
+// The fused epilogue of the wide kernel is not hidden behind MMAs (one
+// accumulator per B tile), that of the narrow one is; a longer reduction makes
+// it a smaller part.  Measured with SiLU (INT8, FP8): K_lp = 5376 narrow 733 us,
+// wide 768; K_lp = 21504 narrow 593, wide 521; equal near 6700.
+constexpr int64_t kFusedWideK = 7168;
+
 // B rows per tile: the whole of a small B, else the largest width <= max.
 int choose_bn(int64_t rowsB, int bn_max) {
     const int64_t r = round_up(rowsB, 32);
     return static_cast<int>(r < bn_max ? r : bn_max);
+}
+
+// B rows per tile of a fused product: choose_bn(), or, where those tiles would
+// leave CTA pairs without one, as few rows (a multiple of 32) as still give
+// every pair at most one tile.  The epilogue's latency then shrinks with the
+// tile: 1000 x 1001 x 650 4:6 INT8 with an fp32 residual (20 tiles of 224 rows,
+// 64 of 64) 22 -> 11 us.
+int choose_bn_fused(int64_t rowsA, int64_t rowsB, int bn_max, int units) {
+    const int bn = choose_bn(rowsB, bn_max);
+    const int64_t nA = (rowsA + 2 * ss::kTileA - 1) / (2 * ss::kTileA);
+    const int64_t per_a = units / nA;  // B tiles that each A tile may have
+    if (per_a <= (rowsB + bn - 1) / bn) return bn;
+    return static_cast<int>(std::min<int64_t>(bn, round_up((rowsB + per_a - 1) / per_a, 32)));
 }
 
 // Groups the GEMM kernels walk the A tiles in (tile_coords).  A wave of CTA
@@ -581,7 +609,9 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
     const int64_t rowsA = sparse_operand == 0 ? N : M;
     const int64_t rowsB = sparse_operand == 0 ? M : N;
     const int pair = rowsA > ss::kTileA ? 2 : 1;
-    const int bn = choose_bn(rowsB, ss::GemmCfg<true, 1>::kBnMax);
+    const int bn = fused ? choose_bn_fused(rowsA, rowsB, ss::GemmCfg<true, 1>::kBnMax,
+                                           g_num_sms[dev] / 2)
+                         : choose_bn(rowsB, ss::GemmCfg<true, 1>::kBnMax);
     if (tiles_overflow(rowsA, rowsB, bn)) return SS_ERR_UNSUPPORTED;
     // operand element bytes: the maps address bytes, so a bf16 row is twice as wide
     const int64_t eb = scaled ? 1 : 2;
@@ -625,8 +655,8 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
     // (8-bit operands only: the bf16 tier runs the one-B-tile kernel)
     // Large problems with bf16 Y may take two B tiles per output tile: fewer
     // bytes per MMA, but single-buffered accumulators.
-    if (scaled && pair == 2 && args.tma_store && forced != 1 &&
-        (forced == 2 || (rowsB > 2 * ss::WideCfg<>::kBnMax &&
+    if (scaled && pair == 2 && args.tma_store && !(fused && !args.a_is_w) && forced != 1 &&
+        (forced == 2 || (rowsB > 2 * ss::WideCfg<>::kBnMax && (!fused || K_lp >= kFusedWideK) &&
                          prefer_wide(rowsA, rowsB, bn, g_num_sms[dev] / 2)))) {
         using CW = ss::WideCfg<>;
         const int bnw = choose_bn_wide(rowsA, rowsB, g_num_sms[dev] / 2);
@@ -640,7 +670,7 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
         wargs.a_groups = a_groups_for(rowsA * (K_lp / 2 + K_lp / 8), (rowsA + 255) / 256,
                                       g_num_sms[dev] / 2, 2 * static_cast<int64_t>(bnw) * K_lp);
         wargs.k_stages = static_cast<int>(K_lp / CW::kStageK);
-        if (fused)  // (TMA stores: channel rows)
+        if (fused)
             return i8 ? launch_gemm_wide<true, true, true>(dev, wa, wb, te, ty, tr, wargs, st_)
                       : launch_gemm_wide<false, true, true>(dev, wa, wb, te, ty, tr, wargs, st_);
         if (args.a_is_w)
@@ -650,7 +680,7 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
                   : launch_gemm_wide<false, false>(dev, wa, wb, te, ty, tr, wargs, st_);
     }
 #endif
-    return dispatch_gemm_any<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, tr, args, st_);
+    return dispatch_gemm<true>(dev, kq, bf, pair, fused, ta, tb, te, ty, tr, args, st_);
 }
 
 // ss_dense_gemm and ss_dense_gemm_fused.
@@ -673,7 +703,8 @@ ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const flo
     int dev;
     if ((st = check_device(&dev)) != SS_OK) return st;
     const int pair = N > ss::kTileA ? 2 : 1;
-    const int bn = choose_bn(M, ss::GemmCfg<false, 1>::kBnMax);
+    const int bn = fused ? choose_bn_fused(N, M, ss::GemmCfg<false, 1>::kBnMax, g_num_sms[dev] / 2)
+                         : choose_bn(M, ss::GemmCfg<false, 1>::kBnMax);
     if (tiles_overflow(N, M, bn)) return SS_ERR_UNSUPPORTED;
     const int64_t eb = scaled ? 1 : 2;  // operand element bytes
     CUtensorMap ta, tb;
@@ -703,7 +734,7 @@ ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const flo
             split(dev, kq, bf, N, M, Wq, K_p * eb, Xq, K_p * eb, ta, args, st_);
         if (sk != SS_ERR_UNSUPPORTED) return sk;
     }
-    return dispatch_gemm_any<false>(dev, kq, bf, pair, fused, ta, tb, ta, ty, tr, args, st_);
+    return dispatch_gemm<false>(dev, kq, bf, pair, fused, ta, tb, ta, ty, tr, args, st_);
 }
 
 }  // namespace
@@ -837,18 +868,10 @@ ss_status gemm_nvfp4(const void* Av, const void* Am, const void* As, const float
     epilogue_maps(ta, Y, M, args.ldy, out_dtype == SS_OUT_BF16, fused, &args, &ty, &tr);
     cudaStream_t st_ = reinterpret_cast<cudaStream_t>(stream);
     const bool bf = out_dtype == SS_OUT_BF16;
-#define SS_FP4_GO(P, E)                                                                       \
-    return bf ? launch_gemm<kSparse, ss::kQNvfp4, true, P, E>(dev, ta, tb, te, ty, tr, args, st_, \
-                                                              &tsa, &tsb)                     \
-              : launch_gemm<kSparse, ss::kQNvfp4, false, P, E>(dev, ta, tb, te, ty, tr, args, \
-                                                               st_, &tsa, &tsb)
-    if (pair == 2) {
-        if (fused) SS_FP4_GO(2, true);
-        SS_FP4_GO(2, false);
-    }
-    if (fused) SS_FP4_GO(1, true);
-    SS_FP4_GO(1, false);
-#undef SS_FP4_GO
+    return pair == 2 ? dispatch_epi<kSparse, ss::kQNvfp4, 2>(dev, bf, fused, ta, tb, te, ty, tr,
+                                                             args, st_, &tsa, &tsb)
+                     : dispatch_epi<kSparse, ss::kQNvfp4, 1>(dev, bf, fused, ta, tb, te, ty, tr,
+                                                             args, st_, &tsa, &tsb);
 }
 
 }  // namespace

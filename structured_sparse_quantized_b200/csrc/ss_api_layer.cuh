@@ -7,28 +7,29 @@
 
 namespace {
 
-template <typename T, int V, bool kHalf>
-ss_status launch_rope(ss::RopeArgs a, cudaStream_t s) {
+template <typename T, int V, int kX, bool kHalf>
+ss_status launch_rope(int dev, ss::RopeArgs a, cudaStream_t s) {
     const int64_t heads = static_cast<int64_t>(a.t[0].heads) + a.t[1].heads;
-    const int pairs = kHalf ? V : (V > 1 ? V / 2 : 1);
-    a.rot_units = a.rot / 2 / pairs;
+    a.rot_units = a.rot / 2 / (kHalf ? kX : kX / 2);
+    a.rest = V > 1 && (a.D - a.rot) % (2 * V) == 0 ? 2 * V : V;
     bool in_place = true;
     for (const ss::RopeTensor& t : a.t)
         in_place = in_place && (t.heads == 0 || (t.in == t.out && t.in_token == t.out_token &&
                                                  t.in_head == t.out_head));
-    a.units = a.rot_units + (in_place ? 0 : (a.D - a.rot) / V);
-    // about four units per thread
+    a.units = a.rot_units + (in_place ? 0 : (a.D - a.rot) / a.rest);
+    // about four units per thread, but at least two blocks per SM
     const int64_t per_token = heads * a.units;
     a.tokens = static_cast<int>(std::min<int64_t>(
-        std::max<int64_t>(4 * ss::kRopeThreads / per_token, 1), ss::kRopeMaxTokens));
-    const size_t smem = static_cast<size_t>(a.tokens) * (a.rot / 2) * sizeof(float2);
+        {std::max<int64_t>(4 * ss::kRopeThreads / per_token, 1), ss::kRopeMaxTokens,
+         std::max<int64_t>(a.T / (2 * g_num_sms[dev]), 1)}));
+    const size_t smem = static_cast<size_t>(a.tokens) * a.rot * sizeof(float);
     const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
-    return launch_ex(ss::rope_kernel<T, V, kHalf>, dim3(grid), dim3(ss::kRopeThreads), smem, s, 1,
-                     a);
+    return launch_ex(ss::rope_kernel<T, V, kX, kHalf>, dim3(grid), dim3(ss::kRopeThreads), smem, s,
+                     1, a);
 }
 
 template <typename T>
-ss_status dispatch_rope(const ss::RopeArgs& a, bool half, cudaStream_t s) {
+ss_status dispatch_rope(int dev, const ss::RopeArgs& a, bool half, cudaStream_t s) {
     // 16-byte accesses need every row start and every unit on a 16-byte boundary
     constexpr int V = 16 / static_cast<int>(sizeof(T));
     bool vec = (a.D - a.rot) % V == 0 && (half ? a.rot / 2 : a.rot) % V == 0;
@@ -37,8 +38,9 @@ ss_status dispatch_rope(const ss::RopeArgs& a, bool half, cudaStream_t s) {
             vec = vec && aligned16(t.in) && aligned16(t.out) && t.in_token % V == 0 &&
                   t.in_head % V == 0 && t.out_token % V == 0 && t.out_head % V == 0;
     if (half)
-        return vec ? launch_rope<T, V, true>(a, s) : launch_rope<T, 1, true>(a, s);
-    return vec ? launch_rope<T, V, false>(a, s) : launch_rope<T, 1, false>(a, s);
+        return vec ? launch_rope<T, V, V, true>(dev, a, s) : launch_rope<T, 1, 1, true>(dev, a, s);
+    if (vec && a.rot % (2 * V) == 0) return launch_rope<T, V, 2 * V, false>(dev, a, s);
+    return vec ? launch_rope<T, V, V, false>(dev, a, s) : launch_rope<T, 1, 2, false>(dev, a, s);
 }
 
 // Bytes of a set's row of codes: 4:6 and 8:10 only, with a chunk past the last group.
@@ -200,8 +202,8 @@ ss_status ss_rope(const ss_rope_heads* q, const ss_rope_heads* k, ss_in_dtype dt
     a.D = static_cast<int>(head_dim);
     a.rot = static_cast<int>(rot_dim);
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    return dtype == SS_IN_BF16 ? dispatch_rope<__nv_bfloat16>(a, layout == SS_ROPE_HALF, s)
-                               : dispatch_rope<float>(a, layout == SS_ROPE_HALF, s);
+    return dtype == SS_IN_BF16 ? dispatch_rope<__nv_bfloat16>(dev, a, layout == SS_ROPE_HALF, s)
+                               : dispatch_rope<float>(dev, a, layout == SS_ROPE_HALF, s);
 }
 
 ss_status ss_norm_quant_lift_act(const void* X, ss_in_dtype in_dtype, const void* weight,

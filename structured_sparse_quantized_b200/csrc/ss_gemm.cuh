@@ -221,13 +221,37 @@ __device__ __forceinline__ void store_scaled(void* y, int64_t off, uint32_t acc_
 // Epilogue of one thread's accumulator row (a_row, columns b0 .. b0 + 15)
 // straight to global memory; sa is the row's scale, sb_lane and bias_lane the
 // scale and (token rows) the bias of column b0 + lane % 16, bias_row the bias
-// of a channel row.
-template <bool kInt8, bool kOutBf16>
-__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uint32_t (&r)[16],
-                                                 int a_row, int b0, float sa, float sb_lane,
-                                                 float bias_row, float bias_lane) {
+// of a channel row.  read(r) delivers the accumulators; the residual's loads
+// are issued before it, and all of them before the first store.
+template <bool kInt8, bool kOutBf16, typename Read>
+__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, int a_row, int b0, float sa,
+                                                 float sb_lane, float bias_row, float bias_lane,
+                                                 Read read) {
     const EpiArgs& e = args.epi;
     const bool row_ok = a_row < args.rowsA;
+    // element u is at off0 + u * stride of Y (and of the residual)
+    const int64_t stride = args.a_is_w ? args.ldy : 1;
+    const int n = row_ok ? min(16, args.rowsB - b0) : 0;
+    // token rows: a thread's 16 (gated: 8) outputs are consecutive, and one by
+    // one they would take a sector each
+    const bool vec = !args.a_is_w && n == 16 && args.ldy % 8 == 0;
+    constexpr int64_t esz = kOutBf16 ? 2 : 4;
+    uint32_t res[16];
+    if (e.residual && !vec) {
+        const int64_t off0 = args.a_is_w ? static_cast<int64_t>(b0) * args.ldy + a_row
+                                         : static_cast<int64_t>(a_row) * args.ldy + b0;
+        if (e.res_f32) {
+            const uint32_t* p = static_cast<const uint32_t*>(e.residual) + off0;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) res[u] = u < n ? p[u * stride] : 0u;
+        } else {
+            const uint16_t* p = static_cast<const uint16_t*>(e.residual) + off0;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) res[u] = u < n ? p[u * stride] : 0u;
+        }
+    }
+    uint32_t r[16];
+    read(r);
     float v[16];
 #pragma unroll
     for (int u = 0; u < 16; ++u) {
@@ -237,20 +261,19 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uin
                    ? fmaf(__fmul_rn(acc, sb), sa, bias_row)
                    : fmaf(__fmul_rn(acc, sa), sb, __shfl_sync(0xffffffffu, bias_lane, u));
     }
-    // element u is at off0 + u * stride of Y (and of the residual)
-    const int64_t stride = args.a_is_w ? args.ldy : 1;
-    const int n = row_ok ? min(16, args.rowsB - b0) : 0;
     if (!e.gated) {
         const int64_t off0 = args.a_is_w ? static_cast<int64_t>(b0) * args.ldy + a_row
                                          : static_cast<int64_t>(a_row) * args.ldy + b0;
         activate<false>(v, e.act);
+        if (vec) {
+            if (e.residual) add_residual_row<16>(e, off0, v);
+            store_row<kOutBf16, 16>(static_cast<uint8_t*>(args.y) + off0 * esz, v);
+            return;
+        }
         if (e.residual) {
-            float res[16];  // every load is issued before the first store
+            const int shift = e.res_f32 ? 0 : 16;  // bf16: the high half of an fp32
 #pragma unroll
-            for (int u = 0; u < 16; ++u)
-                res[u] = u < n ? epi_residual(e, off0 + u * stride) : 0.0f;
-#pragma unroll
-            for (int u = 0; u < 16; ++u) v[u] += res[u];
+            for (int u = 0; u < 16; ++u) v[u] += __uint_as_float(res[u] << shift);
         }
 #pragma unroll
         for (int u = 0; u < 16; ++u)
@@ -272,8 +295,14 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, const uin
         activate<false>(g, e.act);
         const int64_t off0 = static_cast<int64_t>(a_row) * args.ldy + gated_col(b0);
 #pragma unroll
+        for (int u = 0; u < 8; ++u) g[u] *= v[u + 8];
+        if (vec) {
+            store_row<kOutBf16, 8>(static_cast<uint8_t*>(args.y) + off0 * esz, g);
+            return;
+        }
+#pragma unroll
         for (int u = 0; u < 8; ++u)
-            if (u < n) store_y<kOutBf16>(args.y, off0 + u, g[u] * v[u + 8]);
+            if (u < n) store_y<kOutBf16>(args.y, off0 + u, g[u]);
     }
 }
 
@@ -315,11 +344,46 @@ __device__ __forceinline__ float load_b_scale(const float* s, int i, bool in_ran
     else return load_scale<kQ == kQBf16>(s, i, in_range);
 }
 
+// A token row's values at 32 channels from ch0: fma(acc * sa, s_w, bias).  Past
+// the last channel the scale and the bias are 0.
+template <int kQ>
+__device__ __forceinline__ void epi_columns(const GemmArgs& args, int ch0, const uint32_t (&v)[32],
+                                            float sa, float (&y)[32]) {
+    const EpiArgs& e = args.epi;
+    const bool whole = ch0 + 32 <= args.rowsB;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        float s[4], b[4];
+        if (whole && (e.bias_f32 || !e.bias)) {
+            const float4 f = kQ == kQBf16 ? make_float4(1.0f, 1.0f, 1.0f, 1.0f)
+                                          : __ldg(reinterpret_cast<const float4*>(args.s_b + ch0 + i));
+            s[0] = f.x, s[1] = f.y, s[2] = f.z, s[3] = f.w;
+            const float4 g = e.bias ? __ldg(reinterpret_cast<const float4*>(
+                                          static_cast<const float*>(e.bias) + ch0 + i))
+                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            b[0] = g.x, b[1] = g.y, b[2] = g.z, b[3] = g.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool in = ch0 + i + k < args.rowsB;
+                s[k] = load_scale<kQ == kQBf16>(args.s_b, ch0 + i + k, in);
+                b[k] = epi_bias(e, ch0 + i + k, in);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float acc = kQ == kQInt8 ? __int2float_rn(static_cast<int32_t>(v[i + k]))
+                                           : __uint_as_float(v[i + k]);
+            y[i + k] = fmaf(__fmul_rn(acc, sa), s[k], b[k]);
+        }
+    }
+}
+
 // How a warp of the fused epilogue walks a tile's chunks of 32 B rows: chunk j
-// starts at column first + step j of the warp's accumulator part, and its
-// tokens at tile * tile_b_rows + tok_off + that column.
+// starts at column first + step j of the warp's accumulator part, and its B
+// rows at tile * tile_b_rows + b_off + that column.
 struct EpiWalk {
-    int first, step, per_tile, tok_off, tile_b_rows, tile_a_rows, nA, nB;
+    int first, step, per_tile, b_off, tile_b_rows, tile_a_rows, nA, nB;
 };
 
 // What a warp carries from tile to tile: chunks done, and the place of the
@@ -329,14 +393,16 @@ struct EpiState {
     int tile = 0, chunk = 0;
 };
 
-// The fused epilogue of one warp's part of an output tile, A rows = channels
-// and bf16 Y by TMA: 32 channels x 32 tokens at a time through the warp's own
-// staging buffer, with no barrier between warps.
+// The fused epilogue of one warp's part of an output tile, bf16 Y by TMA: 32 A
+// rows x 32 B rows at a time through the warp's own staging buffer of 32 tokens
+// x 32 channels (16 when gated), with no barrier between warps.
 //
-// A thread's 16x256b fragments are channels 16 h + 8 x + lane / 4 of the warp's
+// A rows = channels (kAIsW): a thread's 16x256b fragments are channels 16 h + 8 x + lane / 4 of the warp's
 // 32 and tokens 8 r + 2 (lane % 4) + k: the two factors of a gated output (8
 // channels apart) are its x = 0 and x = 1.  stmatrix.trans turns them into rows
 // of tokens, 64 bytes each (32 when gated), swizzled as the TMA store expects.
+// A rows = tokens: a thread holds its token's 32 channels (tcgen05.ld 32x32b) and
+// writes its own row of the same layout.
 //
 // The residual chunk comes by TMA into the same buffer in the same layout:
 // ldmatrix.trans gives a thread the elements that its stmatrix.trans then
@@ -346,8 +412,8 @@ struct EpiState {
 //
 // tile_at(i): the i-th tile of this cluster (>= n_tiles: none); release gives
 // the accumulator back (one lane).  Returns false when a bounded wait ran out.
-template <int kQ, typename TileAt, typename Release>
-__device__ __forceinline__ bool epi_tile_channels(
+template <int kQ, bool kAIsW, typename TileAt, typename Release>
+__device__ __forceinline__ bool epi_tile_tma(
     const GemmArgs& args, const EpiWalk& walk, EpiState& st, const CUtensorMap& tm_y,
     const CUtensorMap& tm_r, uint8_t* buf, uint64_t* res_full, volatile int* abort_flag,
     int n_tiles, int a_warp0, int b0, int lane, uint32_t t_row, TileAt tile_at, Release release) {
@@ -361,8 +427,9 @@ __device__ __forceinline__ bool epi_tile_channels(
         int ta, tb;
         tile_coords(tile, walk.nA, walk.nB, args.a_groups, ta, tb);
         mbar_arrive_expect_tx(res_full, kFusedWarpBytes);
-        tma_load_2d(buf, &tm_r, res_full, ta * walk.tile_a_rows + a_warp0 % walk.tile_a_rows,
-                    tb * walk.tile_b_rows + walk.tok_off + walk.first + walk.step * st.chunk);
+        const int a = ta * walk.tile_a_rows + a_warp0 % walk.tile_a_rows;
+        const int b = tb * walk.tile_b_rows + walk.b_off + walk.first + walk.step * st.chunk;
+        tma_load_2d(buf, &tm_r, res_full, kAIsW ? a : b, kAIsW ? b : a);
         ++st.issued;
         if (++st.chunk == walk.per_tile) {
             st.chunk = 0;
@@ -379,6 +446,13 @@ __device__ __forceinline__ bool epi_tile_channels(
         const int tok = 8 * (2 * rp + (mi >> 1)) + mj;
         return sy + tok * 64 + (((2 * h + (mi & 1)) ^ ((tok >> 1) & 3)) << 4);
     };
+    // token rows: 16-byte unit i of this thread's row
+    [[maybe_unused]] auto row_unit = [&](int i) {
+        return buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4);
+    };
+    [[maybe_unused]] auto gated_unit = [&](int i) {
+        return buf + lane * 32 + ((i ^ ((lane >> 2) & 1)) << 4);
+    };
     // scales of the fragment's channels (one for the whole tensor in NVFP4) and bias
     constexpr bool kFp4 = kQ == kQNvfp4;
     float sa2[2][2], bias2[2][2];
@@ -386,18 +460,58 @@ __device__ __forceinline__ bool epi_tile_channels(
     for (int h = 0; h < 2; ++h)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            const int ch = a_warp0 + 16 * h + t4 + 8 * x;
+            // (token rows: this thread's row in every place, and no bias of it)
+            const int row = kAIsW ? a_warp0 + 16 * h + t4 + 8 * x : a_warp0 + lane;
             sa2[h][x] = kFp4 ? __ldg(args.s_a)
-                             : load_scale<kQ == kQBf16>(args.s_a, ch, ch < args.rowsA);
-            bias2[h][x] = epi_bias(e, ch, ch < args.rowsA);
+                             : load_scale<kQ == kQBf16>(args.s_a, row, row < args.rowsA);
+            bias2[h][x] = kAIsW ? epi_bias(e, row, row < args.rowsA) : 0.0f;
         }
-    auto read = [&](int c, uint32_t (&v)[32]) {  // [16 h + 4 r + 2 x + k]
+    // channel rows: v[16 h + 4 r + 2 x + k]; token rows: the columns in order
+    auto read = [&](int c, uint32_t (&v)[32]) {
+        if constexpr (!kAIsW) {
+            tmem_ld_32x32b_x32(t_row + c, v);
+            return;
+        }
         tmem_ld_16x256b_x4(t_row + c, *reinterpret_cast<uint32_t(*)[16]>(&v[0]));
         tmem_ld_16x256b_x4(t_row + (16u << 16) + c, *reinterpret_cast<uint32_t(*)[16]>(&v[16]));
     };
     // One chunk: the accumulator v at column c to its packed result, in the
     // order of the staged 8x8 blocks (gated: the first half).
     auto compute = [&](int c, const uint32_t (&v)[32], uint32_t (&pk)[16]) {
+        float y[32];
+        if constexpr (!kAIsW) {
+            epi_columns<kQ>(args, b0 + c, v, sa2[0][0], y);
+            if (e.gated) {
+                float g[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) g[i] = y[((i & 8) << 1) | (i & 7)];
+                activate<false>(g, e.act);
+#pragma unroll
+                for (int i = 0; i < 16; i += 2) {
+                    const int u = (((i & 8) << 1) | (i & 7)) + 8;
+                    pk[i >> 1] = pack_bf16(g[i] * y[u], g[i + 1] * y[u + 1]);
+                }
+                return true;
+            }
+            activate<false>(y, e.act);
+            if (args.tma_res) {
+                const bool got = mbar_wait(res_full, st.n & 1, abort_flag);
+                if (!__all_sync(0xffffffffu, got)) return false;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 u = *reinterpret_cast<const uint4*>(row_unit(i));
+                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        y[8 * i + 2 * k] += __uint_as_float(w[k] << 16);
+                        y[8 * i + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) pk[i >> 1] = pack_bf16(y[i], y[i + 1]);
+            return true;
+        }
         float sb[4][2];
         const int tok = b0 + c + 2 * tm;
         if (kFp4 || kQ == kQBf16) {
@@ -418,7 +532,6 @@ __device__ __forceinline__ bool epi_tile_channels(
                 for (int k = 0; k < 2; ++k)
                     sb[r][k] = tok + 8 * r + k < args.rowsB ? __ldg(args.s_b + tok + 8 * r + k) : 0.0f;
         }
-        float y[32];
 #pragma unroll
         for (int i = 0; i < 32; i += 2) {
             const float x0 = kInt8 ? __int2float_rn(static_cast<int32_t>(v[i]))
@@ -464,7 +577,13 @@ __device__ __forceinline__ bool epi_tile_channels(
             if (lane == 0) bulk_wait_read<0>();  // the last store has read the buffer
             __syncwarp();
         }
-        if (e.gated) {
+        if constexpr (!kAIsW) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (!e.gated || i < 2)
+                    *reinterpret_cast<uint4*>(e.gated ? gated_unit(i) : row_unit(i)) =
+                        make_uint4(pk[4 * i], pk[4 * i + 1], pk[4 * i + 2], pk[4 * i + 3]);
+        } else if (e.gated) {
             const int tok = 8 * mi + mj;  // matrices: r = 0 .. 3 of channel block h
 #pragma unroll
             for (int h = 0; h < 2; ++h)
@@ -480,7 +599,8 @@ __device__ __forceinline__ bool epi_tile_channels(
         __syncwarp();
         ++st.n;
         if (lane == 0) {
-            tma_store_2d_hint(&tm_y, buf, e.gated ? a_warp0 / 2 : a_warp0, b0 + c,
+            const int ch = kAIsW ? a_warp0 : b0 + c;
+            tma_store_2d_hint(&tm_y, buf, e.gated ? ch / 2 : ch, kAIsW ? b0 + c : a_warp0,
                               l2_policy_evict_first());
             bulk_commit_group();
             if (args.tma_res) {
@@ -532,9 +652,10 @@ __device__ __forceinline__ void epi_drain(const EpiState& st, uint64_t* res_full
 
 // kQ: kQE4M3, kQInt8 (kind::f8f6f4 / kind::i8), kQBf16 (kind::f16) or kQNvfp4
 // (kind::mxf4nvf4, block-scaled; tm_sfa / tm_sfb are its scale-factor maps,
-// unused otherwise, and s_a is one global scale).  kEpi: the fused epilogue of
-// args.epi (ss_epilogue.cuh; tm_r is the residual's map, shaped as Y's).
-template <bool kSparse, int kQ, bool kOutBf16, int kPair, bool kEpi = false>
+// unused otherwise, and s_a is one global scale).  kEpi: kEpiNone or the way of
+// the fused epilogue of args.epi (ss_epilogue.cuh; tm_r is the residual's map,
+// shaped as Y's).
+template <bool kSparse, int kQ, bool kOutBf16, int kPair, int kEpi = kEpiNone>
 __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
     gemm_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_e, const __grid_constant__ CUtensorMap tm_y,
@@ -546,8 +667,8 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
     constexpr bool kFp4 = kQ == kQNvfp4;
     constexpr int kEpiWarps = kEpi ? kFusedEpiWarps : kGemmEpiWarps;
     constexpr int kGroups = kEpiWarps / 4;  // of four epilogue warps
-    using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi>,
-                                 GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi>>;
+    using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi != kEpiNone>,
+                                 GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi != kEpiNone>>;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -912,23 +1033,21 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
             const float sa = kFp4 ? __ldg(args.s_a) : load_scale<kBf16>(args.s_a, a_row, row_ok);
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
-            if constexpr (kEpi && kOutBf16) {
-                if (args.tma_store) {  // (channel rows)
-                    const EpiWalk walk = {32 * grp, 32 * kGroups,
-                                          (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups),
-                                          0, args.bn, tile_a_rows, nA, nB};
-                    ok = epi_tile_channels<kQ>(
-                        args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
-                        &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row,
-                        [&](int j) { return unit + j * n_units; },
-                        [&] {
-                            if constexpr (kPair == 2)
-                                mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
-                            else
-                                mbar_arrive(&acc_empty[acc]);
-                        });
-                    continue;
-                }
+            if constexpr (kEpi == kEpiChannels || kEpi == kEpiTokens) {
+                const EpiWalk walk = {32 * grp, 32 * kGroups,
+                                      (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups), 0,
+                                      args.bn, tile_a_rows, nA, nB};
+                ok = epi_tile_tma<kQ, kEpi == kEpiChannels>(
+                    args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
+                    &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row,
+                    [&](int j) { return unit + j * n_units; },
+                    [&] {
+                        if constexpr (kPair == 2)
+                            mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
+                        else
+                            mbar_arrive(&acc_empty[acc]);
+                    });
+                continue;
             }
             if (!kEpi && args.tma_store && args.a_is_w) {
                 // Transposed store path.  Each warp reads its 32 channels x 32
@@ -1061,30 +1180,31 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
             for (int c = 32 * grp; c < args.bn; c += 32 * kGroups) {
                 const int bc = b0 + c + lane;  // this lane's B row of the chunk
                 const float sb_lane = load_b_scale<kQ>(args.s_b, bc, bc < args.rowsB);
-                if constexpr (kEpi) {
+                if constexpr (kEpi == kEpiDirect) {
                     const float bias_row = args.a_is_w ? epi_bias(args.epi, a_row, row_ok) : 0.0f;
                     const float bias_col =
                         args.a_is_w ? 0.0f : epi_bias(args.epi, bc, bc < args.rowsB);
 #pragma unroll 1
                     for (int half = 0; half < 32; half += 16) {
-                        uint32_t r[16];
-                        tmem_ld_32x32b_x16(t_row + c + half, r);
-                        tmem_ld_wait();
-                        if (half == 16 && c + 32 * kGroups >= args.bn) {  // last read: release
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) {
-                                if constexpr (kPair == 2)
-                                    mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));
-                                else
-                                    mbar_arrive(&acc_empty[acc]);
-                            }
-                        }
                         const int from = (lane & 15) + half;
                         epi_store_direct<kInt8, kOutBf16>(
-                            args, r, a_row, b0 + c + half, sa,
+                            args, a_row, b0 + c + half, sa,
                             __shfl_sync(0xffffffffu, sb_lane, from), bias_row,
-                            __shfl_sync(0xffffffffu, bias_col, from));
+                            __shfl_sync(0xffffffffu, bias_col, from), [&](uint32_t (&r)[16]) {
+                                tmem_ld_32x32b_x16(t_row + c + half, r);
+                                tmem_ld_wait();
+                                if (half == 16 && c + 32 * kGroups >= args.bn) {  // last read
+                                    tc_fence_before();
+                                    __syncwarp();
+                                    if (lane == 0) {
+                                        if constexpr (kPair == 2)
+                                            mbar_arrive_cluster(acc_empty_leader +
+                                                                acc * sizeof(uint64_t));
+                                        else
+                                            mbar_arrive(&acc_empty[acc]);
+                                    }
+                                }
+                            });
                     }
                     continue;
                 }

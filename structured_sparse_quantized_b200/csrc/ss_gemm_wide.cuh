@@ -92,7 +92,7 @@ __device__ __forceinline__ int snake_tile(int k, int unit, int n_units) {
 // rows are tokens (activation-sparse, Y[a, b]).
 // kEpi (kAIsW only): the fused epilogue of args.epi (ss_epilogue.cuh; tm_r is
 // the residual's map).  Sixteen warps then take an accumulator chunk by chunk
-// (epi_tile_channels) instead of holding it as packed bf16: what the bias, the
+// (epi_tile_tma) instead of holding it as packed bf16: what the bias, the
 // activation and the residual are added to is not rounded yet.
 template <bool kInt8, bool kAIsW, bool kEpi = false>
 __global__ void __launch_bounds__(kEpi ? kFusedThreads : kWideThreads, 1)
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kWideThreads, 1)
                 const int first = 32 * ((ew >> 2) & 1);  // two groups per B tile
                 const EpiWalk walk = {first, 64, (args.bn - first + 63) / 64, bt * args.bn,
                                       tile_b_rows, kPairRows, nA, nB};
-                const bool done = epi_tile_channels<kInt8 ? kQInt8 : kQE4M3>(
+                const bool done = epi_tile_tma<kInt8 ? kQInt8 : kQE4M3, true>(
                     args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
                     &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, tok0, lane,
                     tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
