@@ -168,7 +168,8 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
                       cudaStream_t stream, const CUtensorMap* sfa = nullptr,
                       const CUtensorMap* sfb = nullptr) {
     using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair, kEpi != 0>,
-                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi != 0>>;
+                                 ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi != 0,
+                                             kEpi == ss::kEpiFew>>;
     auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
@@ -203,6 +204,8 @@ ss_status dispatch_epi(int dev, bool bf16, bool fused, const CUtensorMap& a, con
     if (args.tma_store) {
         if constexpr (kSparse && kQ != kQNvfp4)  // a sparse activation as A: token rows
             if (!args.a_is_w) SS_GEMM_GO(true, kEpiTokens);
+        if constexpr (kPair == 2 && kQ != kQNvfp4)
+            if (args.rowsB <= kFewRows) SS_GEMM_GO(true, kEpiFew);
         SS_GEMM_GO(true, kEpiChannels);
     }
     if (bf16) SS_GEMM_GO(true, kEpiDirect);
@@ -472,7 +475,7 @@ int choose_bn(int64_t rowsB, int bn_max) {
 // leave CTA pairs without one, as few rows (a multiple of 32) as still give
 // every pair at most one tile.  The epilogue's latency then shrinks with the
 // tile: 1000 x 1001 x 650 4:6 INT8 with an fp32 residual (20 tiles of 224 rows,
-// 64 of 64) 22 -> 11 us.
+// 64 of 64) 22 -> 10 us.
 int choose_bn_fused(int64_t rowsA, int64_t rowsB, int bn_max, int units) {
     const int bn = choose_bn(rowsB, bn_max);
     const int64_t nA = (rowsA + 2 * ss::kTileA - 1) / (2 * ss::kTileA);

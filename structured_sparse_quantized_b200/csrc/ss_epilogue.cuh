@@ -29,6 +29,11 @@ constexpr int kActGeluErf = 4;  // v Phi(v)
 // the registers of the widest, and the TMA ways spill (8192 x 4096 x 4096 with
 // a bias 67 us instead of 64.5).
 constexpr int kEpiNone = 0, kEpiChannels = 1, kEpiTokens = 2, kEpiDirect = 3;
+// kEpiChannels for at most kFewRows tokens: such a product streams the weight,
+// and B tiles this small leave room for a ring of 8 stages instead of 4 (6)
+// (16 tokens, 28672 x 4096 6:8 FP8 gated: 26 -> 22.4 us; weight and selectors 110 MB).
+constexpr int kEpiFew = 4;
+constexpr int kFewRows = 64;
 
 struct EpiArgs {
     const void* bias;      // [N], or null

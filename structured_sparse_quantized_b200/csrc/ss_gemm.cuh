@@ -62,7 +62,7 @@ constexpr int kL2PrefetchStages = 16;  // weight stages a CTA prefetches before 
 constexpr int kTileA = 128;  // A rows per CTA per A tile
 constexpr int kTmemCols = 512;
 
-template <bool kSparse, int kPair, int kEb = 1, bool kEpi = false>
+template <bool kSparse, int kPair, int kEb = 1, bool kEpi = false, bool kFew = false>
 struct GemmCfg {
     // One pipeline stage covers kStageK logical K: for 8-bit operands dense
     // 128 (4 MMAs of K=32) and sparse 256 (4 MMAs of K=64); for bf16 (kEb = 2
@@ -81,7 +81,8 @@ struct GemmCfg {
     // of 32-bit columns: an 8-bit MMA (K=64, 64 selector bits per row) uses a
     // whole pair, a bf16 MMA (K=32, 32 bits) one column of it, picked by the
     // sparsity selector of the instruction descriptor (bits 0-1).
-    static constexpr int kBnMax = kSparse ? 224 : 256;     // MMA N; accumulators + metadata
+    // MMA N; accumulators + metadata.  kFew: at most 64 B rows, for deeper rings
+    static constexpr int kBnMax = kFew ? 64 : (kSparse ? 224 : 256);
     static constexpr int kBRowsMax = kBnMax / kPair;       // B rows held per CTA
     static constexpr int kBAtomBytes = kBRowsMax * 128;
     static constexpr int kBBytes = kBAtoms * kBAtomBytes;
@@ -668,7 +669,8 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
     constexpr int kEpiWarps = kEpi ? kFusedEpiWarps : kGemmEpiWarps;
     constexpr int kGroups = kEpiWarps / 4;  // of four epilogue warps
     using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi != kEpiNone>,
-                                 GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi != kEpiNone>>;
+                                 GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi != kEpiNone,
+                                         kEpi == kEpiFew>>;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1033,11 +1035,11 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
             const float sa = kFp4 ? __ldg(args.s_a) : load_scale<kBf16>(args.s_a, a_row, row_ok);
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
-            if constexpr (kEpi == kEpiChannels || kEpi == kEpiTokens) {
+            if constexpr (kEpi == kEpiChannels || kEpi == kEpiFew || kEpi == kEpiTokens) {
                 const EpiWalk walk = {32 * grp, 32 * kGroups,
                                       (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups), 0,
                                       args.bn, tile_a_rows, nA, nB};
-                ok = epi_tile_tma<kQ, kEpi == kEpiChannels>(
+                ok = epi_tile_tma<kQ, kEpi != kEpiTokens>(
                     args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
                     &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row,
                     [&](int j) { return unit + j * n_units; },
