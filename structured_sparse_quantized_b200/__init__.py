@@ -347,7 +347,7 @@ def sparse_gemm(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: int, q,
                 out_dtype=torch.bfloat16, stream=None, out=None, epilogue=None):
     K_lp = Av.shape[1] * 2
     if epilogue is not None:
-        out = epilogue._out(M, N, out_dtype, Av.device, out)
+        out = epilogue._out(M, N, out_dtype, Av, out, stream)
         ss_sparse_gemm_fused(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, epilogue, out,
                              stream)
         return out
@@ -362,7 +362,7 @@ def dense_gemm(Xq, s_x, Wq, s_w, q, out_dtype=torch.bfloat16, stream=None, out=N
     M, K_p = Xq.shape
     N = Wq.shape[0]
     if epilogue is not None:
-        out = epilogue._out(M, N, out_dtype, Xq.device, out)
+        out = epilogue._out(M, N, out_dtype, Xq, out, stream)
         ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M, N, K_p, q, epilogue, out, stream)
         return out
     if out is None:
@@ -476,7 +476,7 @@ def sparse_gemm_nvfp4(packed, act, M: int, N: int, out_dtype=torch.bfloat16, str
     Xv, Xs, g_x = act
     K_lp = Xv.shape[1] * 2
     if epilogue is not None:
-        out = epilogue._out(M, N, out_dtype, Xv.device, out)
+        out = epilogue._out(M, N, out_dtype, Xv, out, stream)
         ss_sparse_gemm_nvfp4_fused(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, epilogue, out,
                                    stream)
         return out
@@ -492,7 +492,7 @@ def dense_gemm_nvfp4(act, packed, M: int, N: int, out_dtype=torch.bfloat16, stre
     Wv, _, Ws, g_w = packed
     K_p = Xv.shape[1] * 2
     if epilogue is not None:
-        out = epilogue._out(M, N, out_dtype, Xv.device, out)
+        out = epilogue._out(M, N, out_dtype, Xv, out, stream)
         ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M, N, K_p, epilogue, out, stream)
         return out
     if out is None:
@@ -542,6 +542,17 @@ def _raw_stream(stream, index: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+
+
+def _new(like: torch.Tensor, shape, dtype, stream):
+    """A tensor on like's device, allocated for the stream that will write it (so
+    that its memory is reused in that stream's order)."""
+    if stream is None:
+        return like.new_empty(shape, dtype=dtype)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return like.new_empty(shape, dtype=dtype)
 
 
 def _index(t, name: str) -> int:
@@ -617,10 +628,10 @@ class Epilogue:
             raise ValueError(f"act must be one of {sorted(ACTS)}, got {act!r}")
         self.bias, self.act, self.gated, self.residual = bias, act, bool(gated), residual
 
-    def _out(self, M, N, out_dtype, device, out):
+    def _out(self, M, N, out_dtype, like, out, stream):
         if out is not None:
             return out
-        return torch.empty((M, N // 2 if self.gated else N), dtype=out_dtype, device=device)
+        return _new(like, (M, N // 2 if self.gated else N), out_dtype, stream)
 
     def _args(self, M, N, Y):
         """(ss_epilogue, Y's pointer, Y's device), checked against the product's shape."""
@@ -751,8 +762,8 @@ def norm_quant_lift_act(X: torch.Tensor, weight: torch.Tensor, eps: float, patte
     -> (Xq_lift [M, K_lp], s_x [M], or None for the bf16 tier)."""
     if out is None:
         M, K = X.shape
-        out = (torch.empty((M, _pattern_k_lp(pattern, K)[1]), dtype=_vals_dtype(q),
-                           device=X.device), _scales(M, q, X.device))
+        s_x = None if _qdtype(q) == SS_BF16 else _new(X, (M,), torch.float32, stream)
+        out = (_new(X, (M, _pattern_k_lp(pattern, K)[1]), _vals_dtype(q), stream), s_x)
     ss_norm_quant_lift_act(X, weight, eps, pattern, q, out[0], out[1], stream)
     return out
 
@@ -827,8 +838,8 @@ def rope(q: torch.Tensor, k, positions: torch.Tensor, freqs: torch.Tensor, layou
     2 * len(freqs) elements of each head turn; freqs and scale come from
     rope_frequencies.  out = (q, k): in place."""
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+        out = (_new(q, q.shape, q.dtype, stream),
+               None if k is None else _new(k, k.shape, k.dtype, stream))
     ss_rope(q, k, positions, freqs, layout, scale, out[0], out[1], stream)
     return out
 

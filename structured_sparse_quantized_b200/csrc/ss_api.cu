@@ -607,6 +607,8 @@ ss_status sparse_gemm(int sparse_operand, const void* Av, const void* Am, const 
     bool fused;
     ss_status st = check_epilogue(epi, N, &args.epi, &fused);
     if (st != SS_OK) return st;
+    // (the fused epilogue reads scales in vectors)
+    if (fused && scaled && (!aligned16(s_a) || !aligned16(s_b))) return SS_ERR_ALIGNMENT;
     int dev;
     if ((st = check_device(&dev)) != SS_OK) return st;
     const int64_t rowsA = sparse_operand == 0 ? N : M;
@@ -703,6 +705,7 @@ ss_status dense_gemm(const void* Xq, const float* s_x, const void* Wq, const flo
     bool fused;
     ss_status st = check_epilogue(epi, N, &args.epi, &fused);
     if (st != SS_OK) return st;
+    if (fused && scaled && (!aligned16(s_x) || !aligned16(s_w))) return SS_ERR_ALIGNMENT;
     int dev;
     if ((st = check_device(&dev)) != SS_OK) return st;
     const int pair = N > ss::kTileA ? 2 : 1;

@@ -385,6 +385,7 @@ __device__ __forceinline__ void epi_columns(const GemmArgs& args, int ch0, const
 // rows at tile * tile_b_rows + b_off + that column.
 struct EpiWalk {
     int first, step, per_tile, b_off, tile_b_rows, tile_a_rows, nA, nB;
+    int a_off;  // the warp's first A row within a tile
 };
 
 // What a warp carries from tile to tile: chunks done, and the place of the
@@ -393,6 +394,29 @@ struct EpiState {
     uint32_t n = 0, issued = 0;
     int tile = 0, chunk = 0;
 };
+
+// Starts the load of the warp's next residual chunk into its staging buffer, if
+// there is one (lane 0).  tile_at(i): the i-th tile of this cluster (>= n_tiles:
+// none).
+template <bool kAIsW, typename TileAt>
+__device__ __forceinline__ void epi_load_residual(const GemmArgs& args, const EpiWalk& walk,
+                                                  EpiState& st, const CUtensorMap& tm_r,
+                                                  uint8_t* buf, uint64_t* res_full, int n_tiles,
+                                                  TileAt tile_at) {
+    const int tile = tile_at(st.tile);
+    if (tile >= n_tiles || walk.per_tile <= 0) return;
+    int ta, tb;
+    tile_coords(tile, walk.nA, walk.nB, args.a_groups, ta, tb);
+    mbar_arrive_expect_tx(res_full, kFusedWarpBytes);
+    const int a = ta * walk.tile_a_rows + walk.a_off;
+    const int b = tb * walk.tile_b_rows + walk.b_off + walk.first + walk.step * st.chunk;
+    tma_load_2d(buf, &tm_r, res_full, kAIsW ? a : b, kAIsW ? b : a);
+    ++st.issued;
+    if (++st.chunk == walk.per_tile) {
+        st.chunk = 0;
+        ++st.tile;
+    }
+}
 
 // The fused epilogue of one warp's part of an output tile, bf16 Y by TMA: 32 A
 // rows x 32 B rows at a time through the warp's own staging buffer of 32 tokens
@@ -409,10 +433,10 @@ struct EpiState {
 // ldmatrix.trans gives a thread the elements that its stmatrix.trans then
 // overwrites, so nothing else is staged and Y may be the residual.  The next
 // chunk's residual is on its way as soon as the store has read the buffer: the
-// first of a tile's during the MMAs.
+// first of a tile's during the MMAs (the caller starts the first of all).
 //
-// tile_at(i): the i-th tile of this cluster (>= n_tiles: none); release gives
-// the accumulator back (one lane).  Returns false when a bounded wait ran out.
+// release gives the accumulator back (one lane).  Returns false when a bounded
+// wait ran out.
 template <int kQ, bool kAIsW, typename TileAt, typename Release>
 __device__ __forceinline__ bool epi_tile_tma(
     const GemmArgs& args, const EpiWalk& walk, EpiState& st, const CUtensorMap& tm_y,
@@ -422,22 +446,6 @@ __device__ __forceinline__ bool epi_tile_tma(
     const EpiArgs& e = args.epi;
     const int t4 = lane >> 2, tm = lane & 3;
     const uint32_t sy = smem_u32(buf);
-    auto load_residual = [&] {  // lane 0: the warp's next residual chunk
-        const int tile = tile_at(st.tile);
-        if (tile >= n_tiles) return;
-        int ta, tb;
-        tile_coords(tile, walk.nA, walk.nB, args.a_groups, ta, tb);
-        mbar_arrive_expect_tx(res_full, kFusedWarpBytes);
-        const int a = ta * walk.tile_a_rows + a_warp0 % walk.tile_a_rows;
-        const int b = tb * walk.tile_b_rows + walk.b_off + walk.first + walk.step * st.chunk;
-        tma_load_2d(buf, &tm_r, res_full, kAIsW ? a : b, kAIsW ? b : a);
-        ++st.issued;
-        if (++st.chunk == walk.per_tile) {
-            st.chunk = 0;
-            ++st.tile;
-        }
-    };
-    if (args.tma_res && st.issued == 0 && lane == 0) load_residual();
     // blocks of this thread's stmatrix rows: matrix mi, row mj.  Row = token;
     // its 16-byte unit of 8 channels is swizzled by the token as SWIZZLE_64B
     // (32B when gated) does.
@@ -606,7 +614,7 @@ __device__ __forceinline__ bool epi_tile_tma(
             bulk_commit_group();
             if (args.tma_res) {
                 bulk_wait_read<0>();
-                load_residual();
+                epi_load_residual<kAIsW>(args, walk, st, tm_r, buf, res_full, n_tiles, tile_at);
             }
         }
     };
@@ -1003,6 +1011,17 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
         int i = 0;
         bool ok = true;
         [[maybe_unused]] EpiState epi;
+        [[maybe_unused]] const EpiWalk walk = {
+            32 * grp, 32 * kGroups,
+            args.bn > 32 * grp ? (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups) : 0,
+            0, args.bn, tile_a_rows, nA, nB, static_cast<int>(rank) * kTileA + q * 32};
+        [[maybe_unused]] auto tile_at = [&](int j) { return unit + j * n_units; };
+        if constexpr (kEpi != kEpiNone && kEpi != kEpiDirect) {
+            if (args.tma_res && lane == 0)
+                epi_load_residual<kEpi != kEpiTokens>(
+                    args, walk, epi, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
+                    &res_full[ew], n_tiles, tile_at);
+        }
         for (int t = unit; t < n_tiles && ok; t += n_units, ++i) {
             int ta, tb;
             tile_coords(t, nA, nB, args.a_groups, ta, tb);
@@ -1036,13 +1055,9 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
             if constexpr (kEpi == kEpiChannels || kEpi == kEpiFew || kEpi == kEpiTokens) {
-                const EpiWalk walk = {32 * grp, 32 * kGroups,
-                                      (args.bn - 32 * grp + 32 * kGroups - 1) / (32 * kGroups), 0,
-                                      args.bn, tile_a_rows, nA, nB};
                 ok = epi_tile_tma<kQ, kEpi != kEpiTokens>(
                     args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
-                    &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row,
-                    [&](int j) { return unit + j * n_units; },
+                    &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row, tile_at,
                     [&] {
                         if constexpr (kPair == 2)
                             mbar_arrive_cluster(acc_empty_leader + acc * sizeof(uint64_t));

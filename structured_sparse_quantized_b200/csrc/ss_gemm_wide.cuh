@@ -324,6 +324,17 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kWideThreads, 1)
         int i = 0;
         uint32_t chunk_iter = 0;
         [[maybe_unused]] EpiState epi;
+        const int first = kEpi ? 32 * ((ew >> 2) & 1) : 0;  // two groups per B tile
+        [[maybe_unused]] const EpiWalk walk = {
+            first, 64, (args.bn - first + 63) / 64, bt * args.bn, tile_b_rows, kPairRows, nA, nB,
+            static_cast<int>(rank) * kTileA + q * 32};
+        [[maybe_unused]] auto tile_at = [&](int j) { return snake_tile(j, unit, n_units); };
+        if constexpr (kEpi) {
+            if (args.tma_res && lane == 0)
+                epi_load_residual<true>(args, walk, epi, tm_r,
+                                        smem + C::kEpiOffset + ew * kFusedWarpBytes,
+                                        &res_full[ew], n_tiles, tile_at);
+        }
         for (int t = snake_tile(0, unit, n_units); t < n_tiles;
              ++i, t = snake_tile(i, unit, n_units)) {
             int ta, tb_;
@@ -335,15 +346,12 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kWideThreads, 1)
                 const bool ready = mbar_wait(acc_full, static_cast<uint32_t>(i & 1), abort_flag);
                 if (!__all_sync(0xffffffffu, ready)) break;
                 tc_fence_after();
-                const int first = 32 * ((ew >> 2) & 1);  // two groups per B tile
-                const EpiWalk walk = {first, 64, (args.bn - first + 63) / 64, bt * args.bn,
-                                      tile_b_rows, kPairRows, nA, nB};
                 const bool done = epi_tile_tma<kInt8 ? kQInt8 : kQE4M3, true>(
                     args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
                     &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, tok0, lane,
                     tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                         static_cast<uint32_t>(bt * C::kAccStride),
-                    [&](int j) { return snake_tile(j, unit, n_units); },
+                    tile_at,
                     [&] { mbar_arrive_cluster(acc_empty_leader); });
                 if (!done) break;
             } else {

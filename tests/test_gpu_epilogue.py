@@ -193,3 +193,112 @@ def test_another_stream():
     want = ref.epilogue(p.d, b.cpu(), "gelu", False, None, BF)
     for y in ys:
         ref.assert_within(y, *want)
+
+
+@pytest.mark.parametrize("kind", ["torch", "handle"])
+def test_stream_argument(kind):
+    """Results and their memory belong to the stream that is passed."""
+    p = Product(300, 272, 512, "int8", "w")
+    b = dev(torch.randn(272))
+    want = ref.epilogue(p.d, b.cpu(), "silu", False, None, BF)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    (wv, wm, sw), (xv, _, sx) = p.w, p.x
+    ys = [ss.sparse_gemm(0, wv, wm, sw, xv, sx, 300, 272, "int8", BF,
+                         stream=s if kind == "torch" else s.cuda_stream,
+                         epilogue=ss.Epilogue(bias=b, act="silu")) for _ in range(8)]
+    s.synchronize()
+    for y in ys:
+        ref.assert_within(y, *want)
+
+
+def test_two_streams_and_two_graphs_at_once():
+    """Calls in flight on two streams, then two captured graphs that share
+    their inputs, replayed together: nothing is shared but what is read."""
+    p = Product(700, 528, 512, "fp8", "w")
+    r = dev((torch.randn(700, 528, generator=torch.Generator().manual_seed(2))).to(BF))
+    cases = [ss.Epilogue(act="gelu", residual=r), ss.Epilogue(act="silu", gated=True)]
+    wants = [ref.epilogue(p.d, None, "gelu", False, r.cpu(), BF),
+             ref.epilogue(p.d, None, "silu", True, None, BF)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [torch.empty(700, 528, dtype=BF, device="cuda"), torch.empty(700, 264, dtype=BF, device="cuda")]
+    torch.cuda.synchronize()
+    for _ in range(6):
+        for s, e, y in zip(streams, cases, outs):
+            with torch.cuda.stream(s):
+                p.run(e, BF, y)
+    torch.cuda.synchronize()
+    for y, want in zip(outs, wants):
+        ref.assert_within(y, *want)
+    graphs = []
+    for s, e, y in zip(streams, cases, outs):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=s):
+            p.run(e, BF, y)
+        graphs.append(g)
+        y.zero_()
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for y, want in zip(outs, wants):
+        ref.assert_within(y, *want)
+
+
+@pytest.mark.parametrize("kernel", ["narrow", "wide"])
+@pytest.mark.parametrize("form", ["w", "x", "dense"])
+def test_wait_runs_out_then_next_call_is_clean(kernel, form, monkeypatch):
+    """A K stage that is never loaded (a wait that nothing satisfies, limited to
+    20 ms): the call records the timeout, residual loads in flight land, and the
+    next call is right."""
+    if form != "w" and kernel == "wide":
+        pytest.skip("channel rows of a sparse weight only")
+    monkeypatch.setenv("SS_SPARSE_KERNEL", kernel)
+    p = Product(500, 1024, 2048, "int8", form)
+    assert ss.ss_get_device_status() == ss.SS_OK
+    r = dev(torch.randn(500, 1024, generator=torch.Generator().manual_seed(4)).to(BF))
+    e = ss.Epilogue(act="silu", residual=r)
+    try:
+        ss.ss_debug_set_wait_limit(20_000_000)
+        ss.ss_debug_skip_stage(1)
+        p.run(e, BF)
+        assert ss.ss_get_device_status() == ss.SS_ERR_TIMEOUT
+        assert ss.ss_get_device_status() == ss.SS_OK
+    finally:
+        ss.ss_debug_skip_stage(-1)
+        ss.ss_debug_set_wait_limit(4_000_000_000)
+    y = p.run(e, BF)
+    assert ss.ss_get_device_status() == ss.SS_OK
+    ref.assert_within(y, *ref.epilogue(p.d, None, "silu", False, r.cpu(), BF))
+
+
+def test_refusals_on_the_device():
+    p = Product(32, 48, 256, "int8", "w")
+    (wv, wm, sw), (xv, _, sx) = p.w, p.x
+
+    def run(e=ss.Epilogue(act="relu"), M=32, N=48, y=None, w=wv, m=wm, s=sw, x=xv):
+        return ss.sparse_gemm(0, w, m, s, x, sx, M, N, "int8", out=y, epilogue=e)
+    run()
+    bad = [dict(e=ss.Epilogue(bias=torch.zeros(47, device="cuda"))),
+           dict(e=ss.Epilogue(bias=torch.zeros(48, device="cuda", dtype=torch.float16))),
+           dict(e=ss.Epilogue(bias=torch.zeros(48))),
+           dict(e=ss.Epilogue(bias=torch.zeros(96, device="cuda")[::2])),
+           dict(e=ss.Epilogue(residual=torch.zeros(32, 24, device="cuda"))),
+           dict(M=31), dict(N=47), dict(y=torch.empty(32, 24, device="cuda", dtype=BF)),
+           dict(y=torch.empty(32, 48, device="cuda", dtype=torch.float16)), dict(m=wm.flatten()[1:]),
+           dict(w=wv.float()), dict(s=None), dict(s=sw[:-1]), dict(x=xv[:-1])]
+    for kw in bad:
+        with pytest.raises(ValueError):
+            run(**kw)
+    for e, status in ((ss.Epilogue(act="silu", gated=True, residual=torch.zeros(32, 48, device="cuda")),
+                       ss.SS_ERR_UNSUPPORTED),
+                      (ss.Epilogue(bias=torch.zeros(52, device="cuda")[1:49]), ss.SS_ERR_ALIGNMENT)):
+        with pytest.raises(ss.SSError) as err:
+            run(e)
+        assert err.value.status == status
+    q = Product(32, 40, 256, "int8", "w")
+    with pytest.raises(ss.SSError) as err:
+        q.run(ss.Epilogue(act="silu", gated=True), BF)
+    assert err.value.status == ss.SS_ERR_INVALID_ARG

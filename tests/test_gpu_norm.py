@@ -112,3 +112,55 @@ def test_captured_graph():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out[0], want[0]) and torch.equal(out[1], want[1])
+
+
+def test_nothing_past_the_rows_is_written():
+    for M, K, pattern in [(3, 64, "6:8"), (1300, 264, "4:6"), (1300, 4096, "6:8"), (5, 1000, "8:10")]:
+        X, w = rows(M, K, BF)
+        _, _, K_lp = oracle.slide_shape(pattern, K)
+        for tier, dtype in (("int8", torch.uint8), ("bf16", BF)):
+            buf = torch.full((M * K_lp + 4096,), 7, dtype=dtype, device="cuda")
+            s = torch.full((M + 64,), 7.0, device="cuda")
+            out = (buf[:M * K_lp].view(M, K_lp), None if tier == "bf16" else s[:M])
+            ss.norm_quant_lift_act(X.cuda(), w.cuda(), 1e-5, pattern, tier, out=out)
+            assert (buf[M * K_lp:] == 7).all() and (s[M:] == 7.0).all()
+
+
+def test_ties_go_to_the_even_code():
+    """Q z / max|z| on the border between two codes: the quotient is exact, and
+    the even code is taken (max 448, so that a code is z itself)."""
+    z = torch.tensor([448.0, 424.0, 440.0, 17.0, 19.0, 2.125, 2.375, 0.0009765625, 0.0029296875])
+    X = torch.zeros(4, 64)
+    X[:, :9] = z
+    Xq, _ = ss.norm_quant_lift_act(X.to(BF).cuda(), torch.ones(64, device="cuda"), 1e-5, "dense", "fp8")
+    got = Xq.view(torch.float8_e4m3fn).float().cpu()[:, :9]
+    want = torch.tensor([448.0, 416.0, 448.0, 16.0, 20.0, 2.0, 2.5, 0.0, 0.00390625])
+    assert torch.equal(got, want.expand(4, 9))
+    X = torch.zeros(4, 64)
+    X[:, :6] = torch.tensor([254.0, 1.0, 3.0, 5.0, -3.0, 253.0])  # codes z / 2
+    Xq, _ = ss.norm_quant_lift_act(X.to(BF).cuda(), torch.ones(64, device="cuda"), 1e-5, "dense", "int8")
+    assert torch.equal(Xq.view(torch.int8).cpu()[:, :6],
+                       torch.tensor([127, 0, 2, 2, -2, 126], dtype=torch.int8).expand(4, 6))
+
+
+def test_refusals_on_the_device():
+    X, w = rows(4, 64, BF)
+    X, w = X.cuda(), w.cuda()
+    for bad in (dict(X=X[0]), dict(X=X.half()), dict(X=X.t()), dict(weight=w[:32]), dict(weight=w.cpu()),
+                dict(weight=None), dict(weight=w.half()), dict(out=(torch.empty(4, 96, device="cuda"), None))):
+        with pytest.raises(ValueError):
+            ss.norm_quant_lift_act(**({"X": X, "weight": w, "eps": 1e-5, "pattern": "6:8", "q": "int8"} | bad))
+    for bad in (dict(eps=-1.0), dict(pattern="3:4")):
+        with pytest.raises(ss.SSError):
+            ss.norm_quant_lift_act(**({"X": X, "weight": w, "eps": 1e-5, "pattern": "6:8", "q": "int8"} | bad))
+
+
+def test_stream_argument():
+    X, w = rows(300, 4096, BF)
+    s = torch.cuda.Stream()
+    x, wc = X.cuda(), w.cuda()
+    s.wait_stream(torch.cuda.current_stream())
+    got = ss.norm_quant_lift_act(x, wc, 1e-5, "6:8", "int8", stream=s)
+    s.synchronize()
+    want = ss.norm_quant_lift_act(x, wc, 1e-5, "6:8", "int8")
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])

@@ -141,3 +141,43 @@ def test_captured_graph():
     torch.cuda.synchronize()
     for y, x in zip(out, (q, k)):
         ref.assert_within(y, *ref.rope(x, new, f.cpu().numpy(), "half", s))
+
+
+def test_refusals_on_the_device():
+    _, q, k, pos = make(8, 4, 2, 64, BF)
+    f, s = ss.rope_frequencies(64)
+    p = pos.cuda()
+    for bad in (dict(q=q[:4]), dict(k=k.float()), dict(k=k[:, :, :32]), dict(positions=p[:4]),
+                dict(positions=p.float()), dict(positions=pos), dict(freqs=f.float()), dict(freqs=f.cpu()),
+                dict(q=q.half()), dict(q=q.transpose(1, 2)), dict(q=q[0]),
+                dict(out=(torch.empty(8, 4, 64, device="cuda", dtype=BF), None)),
+                dict(out=(torch.empty(1, 1, 64, device="cuda", dtype=BF).expand(8, 4, 64), k))):
+        with pytest.raises(ValueError):
+            ss.rope(**({"q": q, "k": k, "positions": p, "freqs": f} | bad))
+    with pytest.raises(ss.SSError):  # more frequencies than pairs
+        ss.rope(q, k, p, torch.ones(33, dtype=torch.float64, device="cuda"))
+    with pytest.raises(ss.SSError):
+        ss.rope(q[:0], None, p[:0], f)
+
+
+def test_one_token_any_strides():
+    """With one token its stride means nothing, whatever it says."""
+    x = torch.randn(2, 64, generator=torch.Generator().manual_seed(1)).to(BF).cuda()
+    q = x.as_strided((1, 2, 64), (7, 64, 1))
+    f, s = ss.rope_frequencies(64)
+    pos = torch.tensor([5])
+    got, _ = ss.rope(q, None, pos.cuda(), f)
+    ref.assert_within(got, *ref.rope(q, pos, f.cpu().numpy(), "half", s))
+
+
+def test_stream_argument():
+    _, q, k, pos = make(64, 8, 2, 128, BF)
+    f, sc = ss.rope_frequencies(128)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    p = pos.cuda()
+    s.wait_stream(torch.cuda.current_stream())
+    got = ss.rope(q, k, p, f, stream=s)
+    s.synchronize()
+    for y, x in zip(got, (q, k)):
+        ref.assert_within(y, *ref.rope(x, pos, f.cpu().numpy(), "half", sc))

@@ -43,6 +43,12 @@ def test_epilogue_refusals(L):
     assert every_gemm(L, epi(gated=1, residual=GOOD)) == {ss.SS_ERR_UNSUPPORTED}
     assert every_gemm(L, epi(bias=ODD)) == {ss.SS_ERR_ALIGNMENT}
     assert every_gemm(L, epi(residual=ODD)) == {ss.SS_ERR_ALIGNMENT}
+    # scales are read in vectors by a fused product
+    for sa, sb in ((ODD, GOOD), (GOOD, ODD)):
+        assert L.ss_sparse_gemm_fused(0, GOOD, GOOD, sa, GOOD, sb, 16, 64, 128, 0, epi(act=1), GOOD, 1,
+                                      None) == ss.SS_ERR_ALIGNMENT
+        assert L.ss_dense_gemm_fused(GOOD, sa, GOOD, sb, 16, 64, 128, 0, epi(act=1), GOOD, 1,
+                                     None) == ss.SS_ERR_ALIGNMENT
     # the plain calls' own checks come first
     assert every_gemm(L, epi(act=1), y=None) == {bad}
     assert every_gemm(L, epi(act=1), y=ODD) == {ss.SS_ERR_ALIGNMENT}
