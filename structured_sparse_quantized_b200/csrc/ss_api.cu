@@ -507,10 +507,12 @@ bool tiles_overflow(int64_t rowsA, int64_t rowsB, int bn) {
     return (rowsA + 127) / 128 * ((rowsB + bn - 1) / bn) > INT32_MAX;
 }
 
-// Opt a row kernel into more than 48 KB of dynamic shared memory when needed.
+// Opt a row kernel into more than 48 KB of shared memory when needed.  The
+// limit without that counts the kernel's static shared memory too (at most 2 KB
+// in these kernels).
 template <typename Kern>
 ss_status set_smem(Kern kern, int /*dev*/, size_t bytes) {
-    if (bytes <= 48 * 1024) return SS_OK;
+    if (bytes <= 46 * 1024) return SS_OK;
     return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 static_cast<int>(bytes)) == cudaSuccess
                ? SS_OK

@@ -99,9 +99,9 @@ ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps
                         M >= 8 * static_cast<int64_t>(g_num_sms[dev]);
     if (stream) {
         if (K <= 512) SS_NORM_STREAM(1, 1);
-        if (K <= 1024) SS_NORM_STREAM(1, 2);
-        if (K <= 2048) SS_NORM_STREAM(1, 4);
-        if (K <= 4096) SS_NORM_STREAM(1, 8);
+        if (K <= 1024) SS_NORM_STREAM(2, 1);
+        if (K <= 2048) SS_NORM_STREAM(2, 2);
+        if (K <= 4096) SS_NORM_STREAM(2, 4);
         if (K <= 8192) SS_NORM_STREAM(2, 8);
     }
     if (K <= 512) SS_NORM_REG(1, 1);

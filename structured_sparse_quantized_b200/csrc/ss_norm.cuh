@@ -72,7 +72,7 @@ __device__ __forceinline__ uint32_t norm_codes4(float p0, float p1, float p2, fl
     } else {
         const uint32_t l = __nv_cvt_float2_to_fp8x2(make_float2(p0, p1), __NV_SATFINITE, __NV_E4M3);
         const uint32_t h = __nv_cvt_float2_to_fp8x2(make_float2(p2, p3), __NV_SATFINITE, __NV_E4M3);
-        return (l & 0xFFFFu) | (h << 16);
+        return __byte_perm(l, h, 0x5410);
     }
 }
 
@@ -311,6 +311,7 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
     float f[kChunks][16];
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
+    const bool whole = s.K == 512 * kChunks * kWpr;  // every thread's chunks are whole
     uint32_t it = 0;
     for (int64_t m = m0; m < M; m += step, ++it) {
         const uint32_t b = it % kNormSlots;
@@ -324,7 +325,7 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
             constexpr int kVec = 16 / static_cast<int>(sizeof(T));
 #pragma unroll
             for (int j = 0; j < 16 / kVec; ++j) {  // K is whole 16-byte words
-                const uint4 u = c * 16 + (j + 1) * kVec <= s.K ? v[j] : make_uint4(0, 0, 0, 0);
+                const uint4 u = whole || c * 16 + (j + 1) * kVec <= s.K ? v[j] : make_uint4(0, 0, 0, 0);
                 const uint32_t uw[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
