@@ -519,23 +519,16 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
 # call, and run on the device of their tensors, on its current stream, whatever
 # device is current.
 
-class _On:
-    """Makes device `index` current for a call, and `old` again after it."""
-
-    def __init__(self, index: int, old: int):
-        self.index, self.old = index, old
-
-    def __enter__(self):
-        if self.index != self.old:
-            torch.cuda.set_device(self.index)
-
-    def __exit__(self, *_):
-        if self.index != self.old:
-            torch.cuda.set_device(self.old)
-
-
-def _on(index: int) -> _On:
-    return _On(index, torch.cuda.current_device())
+def _call(where: str, index: int, *args) -> None:
+    """The C function `where`, with device `index` current."""
+    fn = getattr(lib(), where)
+    if torch._C._cuda_getDevice() == index:
+        status = fn(*args)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args)
+    if status != SS_OK:
+        raise SSError(status, where)
 
 
 def _raw_stream(stream, index: int) -> int:
@@ -567,10 +560,13 @@ def _arg(t, name: str, shape, dtypes, index: int):
     shape (None: any) and one of the types; None stays None."""
     if t is None:
         return None
-    if _index(t, name) == index and t.is_contiguous() and (shape is None or t.shape == shape) \
-            and t.dtype in dtypes:
-        return t.data_ptr()
-    if t.get_device() != index:
+    try:
+        if t.get_device() == index and t.dtype in dtypes and (shape is None or t.shape == shape) \
+                and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    if _index(t, name) != index:
         raise ValueError(f"{name} is on cuda:{t.get_device()}, not cuda:{index}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -670,10 +666,8 @@ def ss_sparse_gemm_fused(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: in
     m = _bytes_arg(Am, "Am", (rows_a + 127) // 128 * 16 * K_lp, d)
     b = _need(B, "B", (rows_b, K_lp), vals, d)
     sa, sb = _scale_arg(s_a, "s_a", rows_a, q, d), _scale_arg(s_b, "s_b", rows_b, q, d)
-    with _on(d):
-        _check(lib().ss_sparse_gemm_fused(sparse_operand, a, m, sa, b, sb, M, N, K_lp, q,
-                                          ctypes.byref(e), y, _out_dtype(Y),
-                                          _raw_stream(stream, d)), "ss_sparse_gemm_fused")
+    _call("ss_sparse_gemm_fused", d, sparse_operand, a, m, sa, b, sb, M, N, K_lp, q,
+          ctypes.byref(e), y, _out_dtype(Y), _raw_stream(stream, d))
 
 
 def ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M: int, N: int, K_p: int, q, epilogue: Epilogue, Y,
@@ -683,10 +677,8 @@ def ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M: int, N: int, K_p: int, q, epilogue:
     vals = _STORED_BF16 if q == SS_BF16 else _STORED_8BIT
     x, w = _need(Xq, "Xq", (M, K_p), vals, d), _need(Wq, "Wq", (N, K_p), vals, d)
     sx, sw = _scale_arg(s_x, "s_x", M, q, d), _scale_arg(s_w, "s_w", N, q, d)
-    with _on(d):
-        _check(lib().ss_dense_gemm_fused(x, sx, w, sw, M, N, K_p, q, ctypes.byref(e), y,
-                                         _out_dtype(Y), _raw_stream(stream, d)),
-               "ss_dense_gemm_fused")
+    _call("ss_dense_gemm_fused", d, x, sx, w, sw, M, N, K_p, q, ctypes.byref(e), y,
+          _out_dtype(Y), _raw_stream(stream, d))
 
 
 def _fp4_scales(s, name, rows, K_lp, block, d):
@@ -708,10 +700,8 @@ def ss_sparse_gemm_nvfp4_fused(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M: int, N: int, K_l
             _fp4_scales(Ws, "Ws", N, K_lp, 32, d), _global_scale(g_w, "g_w", d),
             _need(Xv, "Xv", (M, K_lp // 2), _BYTES, d), _fp4_scales(Xs, "Xs", M, K_lp, 32, d),
             _global_scale(g_x, "g_x", d))
-    with _on(d):
-        _check(lib().ss_sparse_gemm_nvfp4_fused(*args, M, N, K_lp, ctypes.byref(e), y,
-                                                _out_dtype(Y), _raw_stream(stream, d)),
-               "ss_sparse_gemm_nvfp4_fused")
+    _call("ss_sparse_gemm_nvfp4_fused", d, *args, M, N, K_lp, ctypes.byref(e), y,
+          _out_dtype(Y), _raw_stream(stream, d))
 
 
 def ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M: int, N: int, K_p: int,
@@ -720,10 +710,8 @@ def ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M: int, N: int, K_p: int
     args = (_need(Xv, "Xv", (M, K_p // 2), _BYTES, d), _fp4_scales(Xs, "Xs", M, K_p, 16, d),
             _global_scale(g_x, "g_x", d), _need(Wv, "Wv", (N, K_p // 2), _BYTES, d),
             _fp4_scales(Ws, "Ws", N, K_p, 16, d), _global_scale(g_w, "g_w", d))
-    with _on(d):
-        _check(lib().ss_dense_gemm_nvfp4_fused(*args, M, N, K_p, ctypes.byref(e), y,
-                                               _out_dtype(Y), _raw_stream(stream, d)),
-               "ss_dense_gemm_nvfp4_fused")
+    _call("ss_dense_gemm_nvfp4_fused", d, *args, M, N, K_p, ctypes.byref(e), y,
+          _out_dtype(Y), _raw_stream(stream, d))
 
 
 def interleave_gate_up(gate: torch.Tensor, up: torch.Tensor) -> torch.Tensor:
@@ -750,10 +738,8 @@ def ss_norm_quant_lift_act(X, weight, eps: float, pattern, q, Xq_lift, s_x, stre
     w = _need(weight, "weight", (K,), _FLOATS, d)
     xq = _need(Xq_lift, "Xq_lift", (M, K_lp), _STORED_BF16 if q == SS_BF16 else _STORED_8BIT, d)
     sx = _scale_arg(s_x, "s_x", M, q, d)
-    with _on(d):
-        _check(lib().ss_norm_quant_lift_act(x, _IN[X.dtype], w, _IN[weight.dtype], eps, M, K, p, q,
-                                            xq, sx, _raw_stream(stream, d)),
-               "ss_norm_quant_lift_act")
+    _call("ss_norm_quant_lift_act", d, x, _IN[X.dtype], w, _IN[weight.dtype], eps, M, K, p, q,
+          xq, sx, _raw_stream(stream, d))
 
 
 def norm_quant_lift_act(X: torch.Tensor, weight: torch.Tensor, eps: float, pattern, q,
@@ -795,18 +781,20 @@ def rope_frequencies(rot_dim: int, base: float = 10000.0, kind: str = "none", fa
 
 
 def _heads(x, y, name, T, D, dtype, d) -> ss_rope_heads:
-    for t, what in ((x, name), (y, f"{name}'s output")):
-        if _index(t, what) != d or t.dtype != dtype:
-            raise ValueError(f"{what} must be {dtype} on cuda:{d}, like q")
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D or y.shape != x.shape:
-        raise ValueError(f"{name} and its output must be [{T}, heads, {D}], got {tuple(x.shape)} "
-                         f"and {tuple(y.shape)}")
-    (st, sh, se), (ot, oh, oe), H = x.stride(), y.stride(), x.shape[1]
+    if not isinstance(x, torch.Tensor) or not isinstance(y, torch.Tensor):
+        raise ValueError(f"{name} and its output must be CUDA tensors")
+    sx, sy = x.shape, y.shape
+    if not (x.get_device() == d == y.get_device() and x.dtype == dtype == y.dtype):
+        raise ValueError(f"{name} and its output must be {dtype} on cuda:{d}, like q")
+    if len(sx) != 3 or sx[0] != T or sx[2] != D or sx != sy:
+        raise ValueError(f"{name} and its output must be [{T}, heads, {D}], got {tuple(sx)} "
+                         f"and {tuple(sy)}")
+    (st, sh, se), (ot, oh, oe) = x.stride(), y.stride()
     if se != 1 or oe != 1:
         raise ValueError(f"{name}: the elements of a head must be contiguous")
-    if (T > 1 and abs(ot) < 1) or (H > 1 and abs(oh) < 1):
+    if (T > 1 and ot < 1) or (sx[1] > 1 and oh < 1):
         raise ValueError(f"{name}'s output: its elements overlap")
-    return ss_rope_heads(x.data_ptr(), y.data_ptr(), H, st, sh, ot, oh)
+    return ss_rope_heads(x.data_ptr(), y.data_ptr(), sx[1], st, sh, ot, oh)
 
 
 def ss_rope(q, k, positions, freqs, layout, scale: float, q_out, k_out, stream=None) -> None:
@@ -821,10 +809,8 @@ def ss_rope(q, k, positions, freqs, layout, scale: float, q_out, k_out, stream=N
     hk = None if k is None else ctypes.byref(_heads(k, k_out, "k", T, D, q.dtype, d))
     pos = _need(positions, "positions", (T,), _INTS, d)
     f = _need(freqs, "freqs", None, _F64, d)
-    with _on(d):
-        _check(lib().ss_rope(ctypes.byref(hq), hk, _IN[q.dtype], pos,
-                             positions.dtype == torch.int64, f, scale, T, D, 2 * freqs.numel(),
-                             layout, _raw_stream(stream, d)), "ss_rope")
+    _call("ss_rope", d, ctypes.byref(hq), hk, _IN[q.dtype], pos, positions.dtype == torch.int64, f,
+          scale, T, D, 2 * freqs.numel(), layout, _raw_stream(stream, d))
 
 
 _INTS = (torch.int32, torch.int64)
