@@ -37,7 +37,8 @@
 //                chunks: tcgen05.ld the accumulator (lane = A row, column =
 //                B row), scale, convert, stage the chunk in the group's
 //                shared-memory buffer and write it with one TMA tensor store;
-//                release the accumulator on the leader's barrier.
+//                release the accumulator on the leader's barrier.  (With the
+//                fused epilogue of ss_epilogue.cuh: warps 2-17, each on its own.)
 // Every wait is bounded (ss_common.cuh); no load multicasts.
 #pragma once
 
