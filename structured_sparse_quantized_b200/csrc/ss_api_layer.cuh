@@ -28,19 +28,37 @@ ss_status launch_rope(int dev, ss::RopeArgs a, cudaStream_t s) {
                      1, a);
 }
 
+// The widest word (V elements: 16, 8 or 4 bytes, or one element) on whose
+// boundaries every row start and every unit lie.
 template <typename T>
 ss_status dispatch_rope(int dev, const ss::RopeArgs& a, bool half, cudaStream_t s) {
-    // 16-byte accesses need every row start and every unit on a 16-byte boundary
+    int64_t all = 16 / static_cast<int64_t>(sizeof(T));  // then gcd with every offset, in elements
+    auto meet = [&](int64_t n) {
+        while (all > 1 && n % all != 0) all /= 2;
+    };
+    meet(a.D - a.rot);
+    meet(half ? a.rot / 2 : a.rot);
+    for (const ss::RopeTensor& t : a.t) {
+        if (!t.heads) continue;
+        meet(static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.in) / sizeof(T)));
+        meet(static_cast<int64_t>(reinterpret_cast<uintptr_t>(t.out) / sizeof(T)));
+        if (a.T > 1) meet(t.in_token), meet(t.out_token);
+        if (t.heads > 1) meet(t.in_head), meet(t.out_head);
+    }
     constexpr int V = 16 / static_cast<int>(sizeof(T));
-    bool vec = (a.D - a.rot) % V == 0 && (half ? a.rot / 2 : a.rot) % V == 0;
-    for (const ss::RopeTensor& t : a.t)
-        if (t.heads)
-            vec = vec && aligned16(t.in) && aligned16(t.out) && t.in_token % V == 0 &&
-                  t.in_head % V == 0 && t.out_token % V == 0 && t.out_head % V == 0;
-    if (half)
-        return vec ? launch_rope<T, V, V, true>(dev, a, s) : launch_rope<T, 1, 1, true>(dev, a, s);
-    if (vec && a.rot % (2 * V) == 0) return launch_rope<T, V, 2 * V, false>(dev, a, s);
-    return vec ? launch_rope<T, V, V, false>(dev, a, s) : launch_rope<T, 1, 2, false>(dev, a, s);
+    if (half) {
+        if (all == V) return launch_rope<T, V, V, true>(dev, a, s);
+        if (all == V / 2) return launch_rope<T, V / 2, V / 2, true>(dev, a, s);
+        if constexpr (V == 8)
+            if (all == 2) return launch_rope<T, 2, 2, true>(dev, a, s);
+        return launch_rope<T, 1, 1, true>(dev, a, s);
+    }
+    if (all == V && a.rot % (2 * V) == 0) return launch_rope<T, V, 2 * V, false>(dev, a, s);
+    if (all == V) return launch_rope<T, V, V, false>(dev, a, s);
+    if (all == V / 2) return launch_rope<T, V / 2, V / 2, false>(dev, a, s);
+    if constexpr (V == 8)
+        if (all == 2) return launch_rope<T, 2, 2, false>(dev, a, s);
+    return launch_rope<T, 1, 2, false>(dev, a, s);
 }
 
 // Bytes of a set's row of codes: 4:6 and 8:10 only, with a chunk past the last group.
@@ -103,6 +121,8 @@ ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps
         if (K <= 2048) SS_NORM_STREAM(2, 2);
         if (K <= 4096) SS_NORM_STREAM(2, 4);
         if (K <= 8192) SS_NORM_STREAM(2, 8);
+        // (four rows and a code row in flight have to fit shared memory)
+        if (K <= 16384 && K * static_cast<int64_t>(sizeof(T)) <= 32768) SS_NORM_STREAM(4, 8);
     }
     if (K <= 512) SS_NORM_REG(1, 1);
     if (K <= 2048) SS_NORM_REG(1, 4);

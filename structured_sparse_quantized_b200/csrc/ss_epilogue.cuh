@@ -6,11 +6,11 @@
 //   gated:  Y[m, 8 g + i]   = act(v[m, 16 g + i]) * v[m, 16 g + 8 + i],  i < 8
 //
 // all in fp32; without a bias v is the plain product's fp32 value.  A gated
-// weight holds its rows in groups of 16, eight gates
-// and then their eight partners: the two factors of an output then sit 8 rows
-// apart inside one 16-row group, which no kernel shape splits (tiles, K-split
-// reduction slices and tensor-memory lane quarters are multiples of 16), and
-// the 16x256b tensor-memory fragments hold both in one thread.
+// weight holds its rows in groups of 16, eight gates and then their eight
+// partners: the two factors of an output then sit 8 rows apart inside one
+// 16-row group, which no kernel shape splits (tiles, K-split reduction slices
+// and tensor-memory lane quarters are multiples of 16), and the 16x256b
+// tensor-memory fragments hold both in one thread.
 #pragma once
 
 #include "ss_common.cuh"

@@ -356,14 +356,22 @@ __device__ __forceinline__ void epi_columns(const GemmArgs& args, int ch0, const
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
         float s[4], b[4];
-        if (whole && (e.bias_f32 || !e.bias)) {
+        if (whole) {
             const float4 f = kQ == kQBf16 ? make_float4(1.0f, 1.0f, 1.0f, 1.0f)
                                           : __ldg(reinterpret_cast<const float4*>(args.s_b + ch0 + i));
             s[0] = f.x, s[1] = f.y, s[2] = f.z, s[3] = f.w;
-            const float4 g = e.bias ? __ldg(reinterpret_cast<const float4*>(
-                                          static_cast<const float*>(e.bias) + ch0 + i))
-                                    : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            b[0] = g.x, b[1] = g.y, b[2] = g.z, b[3] = g.w;
+            if (!e.bias) {
+                b[0] = b[1] = b[2] = b[3] = 0.0f;
+            } else if (e.bias_f32) {
+                const float4 g = __ldg(reinterpret_cast<const float4*>(
+                    static_cast<const float*>(e.bias) + ch0 + i));
+                b[0] = g.x, b[1] = g.y, b[2] = g.z, b[3] = g.w;
+            } else {
+                const uint2 g = __ldg(reinterpret_cast<const uint2*>(
+                    static_cast<const __nv_bfloat16*>(e.bias) + ch0 + i));
+                b[0] = __uint_as_float(g.x << 16), b[1] = __uint_as_float(g.x & 0xFFFF0000u);
+                b[2] = __uint_as_float(g.y << 16), b[3] = __uint_as_float(g.y & 0xFFFF0000u);
+            }
         } else {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -423,12 +431,12 @@ __device__ __forceinline__ void epi_load_residual(const GemmArgs& args, const Ep
 // rows x 32 B rows at a time through the warp's own staging buffer of 32 tokens
 // x 32 channels (16 when gated), with no barrier between warps.
 //
-// A rows = channels (kAIsW): a thread's 16x256b fragments are channels 16 h + 8 x + lane / 4 of the warp's
-// 32 and tokens 8 r + 2 (lane % 4) + k: the two factors of a gated output (8
-// channels apart) are its x = 0 and x = 1.  stmatrix.trans turns them into rows
-// of tokens, 64 bytes each (32 when gated), swizzled as the TMA store expects.
-// A rows = tokens: a thread holds its token's 32 channels (tcgen05.ld 32x32b) and
-// writes its own row of the same layout.
+// A rows = channels (kAIsW): a thread's 16x256b fragments are channels
+// 16 h + 8 x + lane / 4 of the warp's 32 and tokens 8 r + 2 (lane % 4) + k: the
+// two factors of a gated output (8 channels apart) are its x = 0 and x = 1.
+// stmatrix.trans turns them into rows of tokens, 64 bytes each (32 when gated),
+// swizzled as the TMA store expects.  A rows = tokens: a thread holds its token's
+// 32 channels (tcgen05.ld 32x32b) and writes its own row of the same layout.
 //
 // The residual chunk comes by TMA into the same buffer in the same layout:
 // ldmatrix.trans gives a thread the elements that its stmatrix.trans then

@@ -163,13 +163,13 @@ __device__ __forceinline__ void norm_write_row(const float (&z)[kChunks][16], fl
             }
         } else if constexpr (kBf16) {
             // 6:8: two groups of four words u0..u3, windows (u0 u1) (u1 u2) (u2 u3)
-            uint2* o = reinterpret_cast<uint2*>(out) + 6 * c;
+            uint4* o = reinterpret_cast<uint4*>(out) + 3 * c;
+            const uint4 v[3] = {make_uint4(u[0], u[1], u[1], u[2]),
+                                make_uint4(u[2], u[3], u[4], u[5]),
+                                make_uint4(u[5], u[6], u[6], u[7])};
 #pragma unroll
-            for (int g = 0; g < 2; ++g)
-#pragma unroll
-                for (int j = 0; j < 3; ++j)
-                    if ((6 * c + 3 * g + j) * 8 < row_bytes)
-                        __stcs(o + 3 * g + j, make_uint2(u[4 * g + j], u[4 * g + j + 1]));
+            for (int j = 0; j < 3; ++j)
+                if ((3 * c + j) * 16 < row_bytes) __stcs(o + j, v[j]);
         } else {
             // 6:8: two groups of eight codes, windows at 0, 2, 4 of each
             uint2* o = reinterpret_cast<uint2*>(out) + 3 * c;
@@ -224,6 +224,66 @@ __device__ __forceinline__ void norm_write_row(const float (&z)[kChunks][16], fl
     }
 }
 
+// Elements at, at + 1, ... at + 15 of X (`all` elements, 16-byte aligned), of
+// which the first n are wanted (zero for the rest): from the 16-byte words that
+// hold them, shifted into place.  (16 loads of an element each made 16384 rows of
+// 4095 take 105 us.)
+template <typename T>
+__device__ __forceinline__ void gload16_shifted(const T* __restrict__ X, int64_t at, int n,
+                                                int64_t all, float (&f)[16]) {
+    constexpr int V = 16 / static_cast<int>(sizeof(T));  // elements of a word
+    constexpr int kW = 16 / V + 1;                       // words that may hold 16 elements
+    if (n <= 0) {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+        return;
+    }
+    const int64_t w0 = at / V;
+    const int s = static_cast<int>(at - w0 * V);  // elements before ours in the first word
+    uint32_t x[4 * kW];
+#pragma unroll
+    for (int i = 0; i < kW; ++i) {
+        uint4 v = make_uint4(0, 0, 0, 0);
+        const int64_t first = (w0 + i) * V;
+        if (i * V < s + n) {  // holds an element of ours
+            if (first + V <= all) {
+                v = __ldg(reinterpret_cast<const uint4*>(X) + w0 + i);
+            } else {  // the last word of X, not whole
+                uint32_t p[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+                    if (first + j < all) {
+                        if constexpr (sizeof(T) == 2)
+                            p[j / 2] |= bf16_bits(to_f32<T>(X[first + j])) << (16 * (j & 1));
+                        else
+                            p[j] = __float_as_uint(to_f32<T>(X[first + j]));
+                    }
+                v = make_uint4(p[0], p[1], p[2], p[3]);
+            }
+        }
+        x[4 * i] = v.x, x[4 * i + 1] = v.y, x[4 * i + 2] = v.z, x[4 * i + 3] = v.w;
+    }
+    // move down by s elements: by whole 32-bit words, then by half a word
+    const int words = sizeof(T) == 2 ? s >> 1 : s;
+#pragma unroll
+    for (int i = 0; i < 4 * kW - 2; ++i) x[i] = (words & 2) ? x[i + 2] : x[i];
+#pragma unroll
+    for (int i = 0; i < 4 * kW - 3; ++i) x[i] = (words & 1) ? x[i + 1] : x[i];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+        if constexpr (sizeof(T) == 2) {
+            // element j: half s + j of the words, i.e. (j + (s & 1)) of the moved ones
+            const uint32_t a = x[j / 2], b = x[j / 2 + 1];
+            const uint32_t even = (j & 1) ? a & 0xFFFF0000u : a << 16;
+            const uint32_t odd = (j & 1) ? b << 16 : a & 0xFFFF0000u;
+            f[j] = __uint_as_float((s & 1) ? odd : even);
+        } else {
+            f[j] = __uint_as_float(x[j]);
+        }
+        if (j >= n) f[j] = 0.0f;
+    }
+}
+
 // Rows of up to 512 kChunks kWpr elements, read once: kWpr warps hold a row's
 // z in fp32 registers, 16 kChunks per lane; 8 / kWpr rows per CTA.  For few
 // rows, and for rows that are not whole 16-byte words.
@@ -244,8 +304,13 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
     const int c0 = sub * 32 * kChunks + lane;  // chunks c0 + 32 i, i < kChunks
     float z[kChunks][16];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i)
-        gload16<T>(X + m * s.K, (c0 + 32 * i) * 16, s.K, vec, z[i]);
+    for (int i = 0; i < kChunks; ++i) {
+        const int k = (c0 + 32 * i) * 16;
+        if (vec)
+            gload16<T>(X + m * s.K, k, s.K, true, z[i]);
+        else
+            gload16_shifted<T>(X, m * s.K + k, s.K - k, M * s.K, z[i]);
+    }
     float2 sums = norm_products<kChunks>(z, [&](int i, float (&f)[16]) {
         norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f);
     });
@@ -309,9 +374,13 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
     };
     if (rt == 0)
         for (int b = 0; b < kNormSlots; ++b) issue(m0 + b * step);
-    float f[kChunks][16];
+    // (more than two chunks: from L1 for every row, the registers hold z)
+    constexpr bool kHeld = kChunks <= 2;
+    float f[kHeld ? kChunks : 1][16];
+    if constexpr (kHeld) {
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
+        for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
+    }
     const bool whole = s.K == 512 * kChunks * kWpr;  // every thread's chunks are whole
     uint32_t it = 0;
     for (int64_t m = m0; m < M; m += step, ++it) {
@@ -340,8 +409,12 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
             }
         }
         float2 sums = norm_products<kChunks>(z, [&](int i, float (&g)[16]) {
+            if constexpr (kHeld) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) g[j] = f[i][j];
+                for (int j = 0; j < 16; ++j) g[j] = f[i][j];
+            } else {
+                norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, g);
+            }
         });
         bool all = got;
         if constexpr (kWpr > 1) {

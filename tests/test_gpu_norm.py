@@ -70,7 +70,8 @@ def test_patterns_tiers_sizes(pattern, tier, dtype, M, K):
 @pytest.mark.parametrize("tier", ["int8", "fp8", "bf16"])
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("M,K", [(1500, 4096), (2500, 264), (4003, 1000), (1300, 2040), (1200, 5000),
-                                 (1184, 8), (1200, 4097), (1190, 6144), (1190, 6136)])
+                                 (1184, 8), (1200, 4097), (1190, 6144), (1190, 6136),
+                                 (1184, 16384), (1190, 8200), (1184, 13313)])
 def test_many_rows(pattern, tier, dtype, M, K):
     X, w = rows(M, K, dtype)
     check(X, w.to(BF if M % 2 else F32), 1e-5, pattern, tier)

@@ -36,6 +36,7 @@ def check(q, k, pos, freqs, scale, layout, out=None):
     (1, 32, 8, 128, 128), (64, 28, 4, 128, 128), (257, 5, 5, 64, 64), (33, 16, 2, 80, 32),
     (19, 7, 1, 96, 96), (130, 3, 3, 256, 64), (7, 1, 1, 2, 2), (40, 9, 3, 66, 42),
     (3, 2, 1, 1024, 1022), (5, 64, 64, 72, 72), (70, 3, 1, 104, 72), (31, 2, 2, 64, 24),
+    (40, 4, 2, 96, 40), (33, 5, 1, 128, 90), (50, 2, 2, 68, 36),
 ])
 def test_layouts_and_sizes(layout, dtype, T, Hq, Hk, D, rot):
     _, q, k, pos = make(T, Hq, Hk, D, dtype)
