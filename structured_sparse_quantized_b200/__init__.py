@@ -377,6 +377,9 @@ def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream
     GEMM (or the dense GEMM for pattern 'dense').  `packed` = compress_weight().
     norm = (weight, eps): RMS norm of X fused into the quantisation.
     epilogue: bias, activation and residual fused into the GEMM."""
+    if stream is not None and (epilogue is not None or norm is not None):
+        with _as_current(stream, X):  # the quantised activation is that stream's too
+            return linear(X, packed, pattern, q, out_dtype, None, epilogue, norm, out)
     Wv, Wm, s_w = packed
     M = X.shape[0]
     N = Wv.shape[0]
@@ -506,6 +509,9 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
     """Y = X W^T in NVFP4: quantisation with one global scale for X + pair
     lift (blocks of 32 for a sparse weight, 16 for a dense one), then the
     block-scaled GEMM, with the fused epilogue if one is given."""
+    if stream is not None and epilogue is not None:
+        with _as_current(stream, X):
+            return linear_nvfp4(X, packed, pattern, out_dtype, None, epilogue, out)
     dense = _pattern(pattern).group == 0
     act = quant_lift_act_nvfp4(X, pattern, 16 if dense else 32, stream)
     M, N = X.shape[0], packed[0].shape[0]
@@ -542,10 +548,15 @@ def _new(like: torch.Tensor, shape, dtype, stream):
     that its memory is reused in that stream's order)."""
     if stream is None:
         return like.new_empty(shape, dtype=dtype)
+    with _as_current(stream, like):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _as_current(stream, like: torch.Tensor):
+    """Context in which `stream` (a Stream or a handle) is the current one."""
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-    with torch.cuda.stream(stream):
-        return like.new_empty(shape, dtype=dtype)
+    return torch.cuda.stream(stream)
 
 
 def _index(t, name: str) -> int:
@@ -837,14 +848,18 @@ def project_qkv(X: torch.Tensor, packed, pattern, q, heads: int, kv_heads: int, 
     value product with its bias, and rotary positions on the query and key
     heads in place.  The weight's rows are (heads + 2 kv_heads) heads of equal
     size.  -> q [M, heads, D], k, v [M, kv_heads, D], views of one tensor."""
+    if stream is not None:
+        with _as_current(stream, X):
+            return project_qkv(X, packed, pattern, q, heads, kv_heads, positions, freqs, layout,
+                               scale, norm, bias)
     N = packed[0].shape[0]
     if N % (heads + 2 * kv_heads) != 0:
         raise ValueError(f"{N} rows are not {heads} + 2 * {kv_heads} heads")
-    Y = linear(X, packed, pattern, q, stream=stream, norm=norm,
+    Y = linear(X, packed, pattern, q, norm=norm,
                epilogue=None if bias is None else Epilogue(bias=bias))
     Y = Y.view(X.shape[0], heads + 2 * kv_heads, -1)
     yq, yk, yv = Y.split((heads, kv_heads, kv_heads), dim=1)
-    rope(yq, yk, positions, freqs, layout, scale, stream, out=(yq, yk))
+    rope(yq, yk, positions, freqs, layout, scale, out=(yq, yk))
     return yq, yk, yv
 
 
@@ -854,6 +869,8 @@ def feed_forward(X: torch.Tensor, packed_gate_up, packed_down, pattern, q, act="
     with gate, up of the RMS norm of X (norm = (weight, eps) or None):
     `packed_gate_up` = compress_weight(interleave_gate_up(W_gate, W_up)).
     -> [M, K] of X's type."""
-    h = linear(X, packed_gate_up, pattern, q, stream=stream, norm=norm,
-               epilogue=Epilogue(act=act, gated=True))
-    return linear(h, packed_down, pattern, q, X.dtype, stream, Epilogue(residual=X))
+    if stream is not None:
+        with _as_current(stream, X):
+            return feed_forward(X, packed_gate_up, packed_down, pattern, q, act, norm)
+    h = linear(X, packed_gate_up, pattern, q, norm=norm, epilogue=Epilogue(act=act, gated=True))
+    return linear(h, packed_down, pattern, q, X.dtype, epilogue=Epilogue(residual=X))

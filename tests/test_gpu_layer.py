@@ -64,3 +64,40 @@ def test_layer_path(M, pattern):
     h = (torch.nn.functional.silu(gu[:, :, 0]) * gu[:, :, 1]).reshape(M, F)
     want = rmid + h @ dense_of(pd, pattern, F).t()
     assert rel(out, want) < 0.03
+
+
+@pytest.mark.parametrize("M", [1, 200])
+@pytest.mark.parametrize("dtype", [BF, torch.float32])
+def test_feed_forward_on_a_stream_repeats(M, dtype):
+    """The same call on the current stream and, repeatedly, on another one (its
+    intermediates are reused there while calls are in flight); fp32 stream too."""
+    g = torch.Generator().manual_seed(M)
+    K, F = 256, 352
+    X = torch.randn(M, K, generator=g).to(dtype).cuda()
+    w = torch.ones(K, device="cuda")
+    pg = ss.compress_weight(ss.interleave_gate_up(torch.randn(F, K, generator=g) * 0.06,
+                                                  torch.randn(F, K, generator=g) * 0.06).cuda(), "6:8", "int8")
+    pd = ss.compress_weight((torch.randn(K, F, generator=g) * 0.05).cuda(), "6:8", "int8")
+    want = ss.feed_forward(X, pg, pd, "6:8", "int8", norm=(w, 1e-5))
+    assert want.dtype == dtype
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = [ss.feed_forward(X, pg, pd, "6:8", "int8", norm=(w, 1e-5), stream=s) for _ in range(10)]
+    s.synchronize()
+    for y in got:
+        assert torch.equal(y, want)
+
+
+def test_nvfp4_linear_with_epilogue():
+    """linear_nvfp4's epilogue against the plain call's fp32 output."""
+    g = torch.Generator().manual_seed(3)
+    X, W = torch.randn(70, 512, generator=g).to(BF).cuda(), (torch.randn(272, 512, generator=g) * 0.05).to(BF).cuda()
+    b, r = torch.randn(272, generator=g).cuda(), torch.randn(70, 272, generator=g).to(BF).cuda()
+    for pattern in ("2:4", "dense"):
+        packed = ss.compress_weight_nvfp4(W, pattern)
+        plain = ss.linear_nvfp4(X, packed, pattern, torch.float32).double()
+        v = plain + b.double()
+        want = v * torch.sigmoid(v) + r.double()
+        got = ss.linear_nvfp4(X, packed, pattern, BF, epilogue=ss.Epilogue(bias=b, act="silu", residual=r))
+        # half a step of bf16, and fp32 arithmetic on values of order one
+        assert ((got.double() - want).abs() <= want.abs() * 2.0 ** -8 + 1e-5).all()
