@@ -85,22 +85,25 @@ ss_status launch_norm_reg(const void* X, const void* w, int wf32, float eps, int
 template <typename T, int kQ, int kChunks, int kWpr>
 ss_status launch_norm_stream(int dev, const void* X, const void* w, int wf32, float eps, int64_t M,
                              const ss::NormShape& shape, void* Xq, float* s_x, cudaStream_t s) {
-    constexpr int64_t kSets = ss::kWarpRowThreads / (32 * kWpr);
+    constexpr int kThreads = ss::norm_stream_threads(kWpr);
+    constexpr int64_t kSets = kThreads / (32 * kWpr);
     const int q_stride = norm_code_row(shape, kQ == ss::kQBf16 ? 2 : 1);
     const int slot = static_cast<int>(round_up(shape.K * static_cast<int64_t>(sizeof(T)), 128));
     auto kern = ss::norm_quant_lift_stream_kernel<T, kQ, kChunks, kWpr>;
-    const size_t smem = static_cast<size_t>(kSets) * (ss::kNormSlots * slot + q_stride);
+    const int n_slots = static_cast<int>(std::min<int64_t>(
+        ss::kNormSlots, (static_cast<int64_t>(kMaxRowSmem) / kSets - q_stride) / slot));
+    const size_t smem = static_cast<size_t>(kSets) * (n_slots * slot + q_stride);
     const ss_status st = set_smem(kern, dev, smem);
     if (st != SS_OK) return st;
     int per_sm = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, ss::kWarpRowThreads, smem) !=
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) !=
             cudaSuccess ||
         per_sm < 1)
         return SS_ERR_CUDA;
     const int64_t ctas = std::min<int64_t>((M + kSets - 1) / kSets,
                                            static_cast<int64_t>(per_sm) * g_num_sms[dev]);
-    return launch_ex(kern, dim3(static_cast<unsigned>(ctas)), dim3(ss::kWarpRowThreads), smem, s, 1,
-                     static_cast<const T*>(X), w, wf32, eps, M, shape, slot, q_stride,
+    return launch_ex(kern, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), smem, s, 1,
+                     static_cast<const T*>(X), w, wf32, eps, M, shape, n_slots, slot, q_stride,
                      static_cast<uint8_t*>(Xq), s_x);
 }
 
@@ -121,8 +124,7 @@ ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps
         if (K <= 2048) SS_NORM_STREAM(2, 2);
         if (K <= 4096) SS_NORM_STREAM(2, 4);
         if (K <= 8192) SS_NORM_STREAM(2, 8);
-        // (four rows and a code row in flight have to fit shared memory)
-        if (K <= 16384 && K * static_cast<int64_t>(sizeof(T)) <= 32768) SS_NORM_STREAM(4, 8);
+        if (K <= 16384) SS_NORM_STREAM(2, 16);
     }
     if (K <= 512) SS_NORM_REG(1, 1);
     if (K <= 2048) SS_NORM_REG(1, 4);

@@ -7,11 +7,10 @@
 //
 // The row's factor r cancels in Q y / max|y|: the codes come from z = x w
 // alone, and r enters s_x = r max|z| / Q.  For bf16 x and w the product z is
-// exact, and so is Q z; the quotient Q z / max|z| is rounded correctly (one
-// Newton correction of the product with 1 / max|z|).  Ratios of 16-bit
-// products fall on the border between two codes often (1200 of 16M elements
-// at FP8), and the correctly rounded quotient then goes to the even code, as
-// the definition says, instead of either way.
+// exact, and the quotient Q z / max|z| is formed with Q / max|z| in two parts
+// and rounded once.  Ratios of 16-bit products fall on the border between two
+// codes often (1200 of 16M elements at FP8), and they then go to the even code,
+// as the definition says, instead of either way.
 //
 // The normalised row is never written: X is read and the codes are written,
 // which is all the memory traffic there is.
@@ -329,19 +328,23 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
 // the weights of its chunks in registers and kNormSlots rows in flight from
 // HBM into shared memory (1-D bulk copies), so that the copies of the next
 // rows go on while a row is reduced, quantised and stored.  Bound by HBM: 16384
-// rows of 4096 bf16 to 6:8 FP8 in 43 us, 84% of the measured copy rate.
+// rows of 4096 bf16 to 6:8 FP8 in 44 us, 83% of the measured copy rate.
 // Without the copies in flight (rows straight to registers, 2 to 8 warps per
 // row) 16384 rows of 4096 took 50-89 us: the loads pause in every row's
 // reduction, and a weight read per row costs as much L1 time as the row.
-constexpr int kNormSlots = 4;
+constexpr int kNormSlots = 4;  // at most: as many as fit shared memory
+
+// 256 threads, or one set of sixteen warps (rows past 8192: eight warps would
+// hold too much of a row each to keep its weights too; 5041 x 13312 78 -> 51 us).
+constexpr int norm_stream_threads(int wpr) { return wpr > 8 ? 32 * wpr : kWarpRowThreads; }
 
 template <typename T, int kQ, int kChunks, int kWpr>
-__global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel(
+__global__ void __launch_bounds__(norm_stream_threads(kWpr)) norm_quant_lift_stream_kernel(
     const T* __restrict__ X, const void* __restrict__ w, int wf32, float eps, int64_t M,
-    const NormShape s, int slot_stride, int q_stride, uint8_t* __restrict__ Xq,
+    const NormShape s, int n_slots, int slot_stride, int q_stride, uint8_t* __restrict__ Xq,
     float* __restrict__ s_x) {
     extern __shared__ __align__(16) uint8_t smem_raw[];
-    constexpr int kSets = kWarpRowThreads / (32 * kWpr);
+    constexpr int kSets = norm_stream_threads(kWpr) / (32 * kWpr);
     __shared__ uint64_t full[kSets][kNormSlots];
     __shared__ float2 part[2][kSets][kWpr];
     __shared__ int abort_flag_storage;
@@ -352,40 +355,35 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
     const int c0 = sub * 32 * kChunks + lane;
     if (threadIdx.x == 0) *abort_flag = 0;
     if (rt == 0) {
-        for (int b = 0; b < kNormSlots; ++b) mbar_init(&full[set][b], 1);
+        for (int b = 0; b < n_slots; ++b) mbar_init(&full[set][b], 1);
         fence_barrier_init();
     }
     __syncthreads();
     pdl_trigger();
     pdl_wait();
-    uint8_t* slots = smem_raw + set * (kNormSlots * slot_stride);
-    uint4* qrow = reinterpret_cast<uint4*>(smem_raw + kSets * kNormSlots * slot_stride +
+    uint8_t* slots = smem_raw + set * (n_slots * slot_stride);
+    uint4* qrow = reinterpret_cast<uint4*>(smem_raw + kSets * n_slots * slot_stride +
                                            set * q_stride);
     const uint32_t bytes = static_cast<uint32_t>(s.K) * static_cast<uint32_t>(sizeof(T));
     const int64_t step = static_cast<int64_t>(gridDim.x) * kSets;
     const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kSets + set;
-    uint32_t issued = 0, taken = 0;  // rows copied and awaited (thread 0 of the set)
-    auto issue = [&](int64_t m) {
+    uint32_t pending = 0;  // slots with a copy in flight (thread 0 of the set)
+    auto issue = [&](int64_t m, int b) {
         if (m >= M) return;
-        const uint32_t b = issued % kNormSlots;
+        pending |= 1u << b;
         mbar_arrive_expect_tx(&full[set][b], bytes);
         bulk_load_1d(slots + b * slot_stride, X + m * s.K, bytes, &full[set][b]);
-        ++issued;
     };
     if (rt == 0)
-        for (int b = 0; b < kNormSlots; ++b) issue(m0 + b * step);
-    // (more than two chunks: from L1 for every row, the registers hold z)
-    constexpr bool kHeld = kChunks <= 2;
-    float f[kHeld ? kChunks : 1][16];
-    if constexpr (kHeld) {
+        for (int b = 0; b < n_slots; ++b) issue(m0 + b * step, b);
+    float f[kChunks][16];
 #pragma unroll
-        for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
-    }
+    for (int i = 0; i < kChunks; ++i) norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, f[i]);
     const bool whole = s.K == 512 * kChunks * kWpr;  // every thread's chunks are whole
-    uint32_t it = 0;
-    for (int64_t m = m0; m < M; m += step, ++it) {
-        const uint32_t b = it % kNormSlots;
-        const bool got = mbar_wait(&full[set][b], (it / kNormSlots) & 1, abort_flag);
+    int b = 0;             // slot of this row
+    uint32_t phase = 0, odd = 0;  // parity of the slot's copies, and of the rows
+    for (int64_t m = m0; m < M; m += step, odd ^= 1u) {
+        const bool got = mbar_wait(&full[set][b], phase, abort_flag);
         const T* x = reinterpret_cast<const T*>(slots + b * slot_stride);
         float z[kChunks][16];
 #pragma unroll
@@ -409,36 +407,38 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_stream_kernel
             }
         }
         float2 sums = norm_products<kChunks>(z, [&](int i, float (&g)[16]) {
-            if constexpr (kHeld) {
 #pragma unroll
-                for (int j = 0; j < 16; ++j) g[j] = f[i][j];
-            } else {
-                norm_weight16(w, wf32, (c0 + 32 * i) * 16, s.K, g);
-            }
+            for (int j = 0; j < 16; ++j) g[j] = f[i][j];
         });
         bool all = got;
         if constexpr (kWpr > 1) {
-            if (lane == 0) part[it & 1][set][sub] = sums;
+            if (lane == 0) part[odd][set][sub] = sums;
             // also: every warp of the set has read the slot, and is done with
             // the code row and the parts of two rows ago
             all = named_bar_and(1 + set, 32 * kWpr, got);
-            sums = norm_combine<kWpr>(part[it & 1][set]);
+            sums = norm_combine<kWpr>(part[odd][set]);
         } else {
             all = __all_sync(0xffffffffu, got);
         }
         if (!all) break;
         if (rt == 0) {
-            taken = it + 1;
+            pending &= ~(1u << b);
             fence_async_shared();
-            issue(m + kNormSlots * step);
+            issue(m + n_slots * step, b);
+        }
+        if (++b == n_slots) {
+            b = 0;
+            phase ^= 1u;
         }
         norm_write_row<kQ, kChunks, kWpr>(
             z, sums, eps, s, c0, rt, 1 + set, qrow,
             Xq + m * static_cast<int64_t>(s.K_lp) * (kQ == kQBf16 ? 2 : 1), s_x + m);
     }
-    if (rt == 0)  // after a wait that ran out: copies in flight land before exit
-        for (; taken < issued; ++taken)
-            mbar_drain(&full[set][taken % kNormSlots], (taken / kNormSlots) & 1);
+    // after a wait that ran out: copies in flight land before exit (a slot from b
+    // on waits for this phase, one before b for the next)
+    if (rt == 0 && pending)
+        for (int i = 0; i < n_slots; ++i)
+            if ((pending >> i) & 1u) mbar_drain(&full[set][i], i >= b ? phase : phase ^ 1u);
 }
 
 // One block per token row, any K.  The output is walked in lifted order, each

@@ -66,12 +66,15 @@ def test_patterns_tiers_sizes(pattern, tier, dtype, M, K):
     check(X, w.to(BF if K % 3 else F32), 1e-5, pattern, tier)
 
 
-@pytest.mark.parametrize("pattern", ["dense", "4:6", "6:8", "8:10"])
+MANY = [(p, M, K) for M, K in [(1500, 4096), (2500, 264), (4003, 1000), (1300, 2040), (1184, 8), (1200, 4097)]
+        for p in ("dense", "4:6", "6:8", "8:10")]
+MANY += [(p, M, K) for M, K in [(1200, 5000), (1190, 6144), (1190, 6136), (1184, 16384), (1190, 8200),
+                                (1184, 13313), (1300, 12304)] for p in ("6:8", "8:10")]
+
+
 @pytest.mark.parametrize("tier", ["int8", "fp8", "bf16"])
 @pytest.mark.parametrize("dtype", [BF, F32])
-@pytest.mark.parametrize("M,K", [(1500, 4096), (2500, 264), (4003, 1000), (1300, 2040), (1200, 5000),
-                                 (1184, 8), (1200, 4097), (1190, 6144), (1190, 6136),
-                                 (1184, 16384), (1190, 8200), (1184, 13313)])
+@pytest.mark.parametrize("pattern,M,K", MANY)
 def test_many_rows(pattern, tier, dtype, M, K):
     X, w = rows(M, K, dtype)
     check(X, w.to(BF if M % 2 else F32), 1e-5, pattern, tier)
