@@ -23,9 +23,15 @@ ss_status launch_rope(int dev, ss::RopeArgs a, cudaStream_t s) {
         {std::max<int64_t>(4 * ss::kRopeThreads / per_token, 1), ss::kRopeMaxTokens,
          std::max<int64_t>(a.T / (2 * g_num_sms[dev]), 1)}));
     const size_t smem = static_cast<size_t>(a.tokens) * a.rot * sizeof(float);
-    const unsigned grid = static_cast<unsigned>((a.T + a.tokens - 1) / a.tokens);
-    return launch_ex(ss::rope_kernel<T, V, kX, kHalf>, dim3(grid), dim3(ss::kRopeThreads), smem, s,
-                     1, a);
+    const int64_t blocks = (a.T + a.tokens - 1) / a.tokens;
+    // with too few tokens for that, a token's heads go to several blocks, as long
+    // as each keeps a unit for every thread (every block forms its own cos and sin)
+    const int64_t rows = a.tokens * heads, passes = a.tokens * per_token / ss::kRopeThreads;
+    const int64_t parts = std::max<int64_t>(std::min(passes, 2 * g_num_sms[dev] / blocks), 1);
+    a.rows = static_cast<int>((rows + parts - 1) / parts);
+    return launch_ex(ss::rope_kernel<T, V, kX, kHalf>,
+                     dim3(static_cast<unsigned>(blocks), static_cast<unsigned>(parts)),
+                     dim3(ss::kRopeThreads), smem, s, 1, a);
 }
 
 // The widest word (V elements: 16, 8 or 4 bytes, or one element) on whose

@@ -47,6 +47,7 @@ struct RopeArgs {
     int pos64;                           // 1: int64 positions, 0: int32
     int T, D, rot;
     int tokens;                          // per block
+    int rows;                            // (token, head) rows per blockIdx.y
     int units;                           // work units per head
     int rot_units;                       // of them, units that rotate
     int rest;                            // elements of a unit past rot
@@ -141,9 +142,11 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeArgs a) {
     }
     __syncthreads();
     const int heads = a.t[0].heads + a.t[1].heads;
-    const int n_rows = n_tok * heads;
+    const int row0 = static_cast<int>(blockIdx.y) * a.rows;
+    const int n_rows = min(row0 + a.rows, n_tok * heads);
     const int units = a.units, du = kRopeThreads % units, dr = kRopeThreads / units;
     int row = static_cast<int>(threadIdx.x) / units, u = static_cast<int>(threadIdx.x) - row * units;
+    row += row0;
     int tk = row / heads, h = row - tk * heads;
     while (row < n_rows) {
         const int k = h < a.t[0].heads ? 0 : 1;
