@@ -169,7 +169,7 @@ ss_status launch_gemm(int dev, const CUtensorMap& a, const CUtensorMap& b, const
                       const CUtensorMap* sfb = nullptr) {
     using C = std::conditional_t<kQ == ss::kQNvfp4, ss::Fp4Cfg<kSparse, kPair, kEpi != 0>,
                                  ss::GemmCfg<kSparse, kPair, kQ == ss::kQBf16 ? 2 : 1, kEpi != 0,
-                                             kEpi == ss::kEpiFew>>;
+                                             ss::epi_is_few(kEpi)>>;
     auto kern = ss::gemm_kernel<kSparse, kQ, kOutBf16, kPair, kEpi>;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_err[kMaxDevices];
@@ -202,10 +202,15 @@ ss_status dispatch_epi(int dev, bool bf16, bool fused, const CUtensorMap& a, con
         SS_GEMM_GO(false, kEpiNone);
     }
     if (args.tma_store) {
-        if constexpr (kSparse && kQ != kQNvfp4)  // a sparse activation as A: token rows
-            if (!args.a_is_w) SS_GEMM_GO(true, kEpiTokens);
-        if constexpr (kPair == 2 && kQ != kQNvfp4)
-            if (args.rowsB <= kFewRows) SS_GEMM_GO(true, kEpiFew);
+        [[maybe_unused]] const bool few = args.bn <= kFewRows;
+        if constexpr (kSparse && kQ != kQNvfp4) {  // a sparse activation as A: token rows
+            if (!args.a_is_w) {
+                if (few) SS_GEMM_GO(true, kEpiTokensFew);
+                SS_GEMM_GO(true, kEpiTokens);
+            }
+        }
+        if constexpr (kQ != kQNvfp4)
+            if (few) SS_GEMM_GO(true, kEpiChannelsFew);
         SS_GEMM_GO(true, kEpiChannels);
     }
     if (bf16) SS_GEMM_GO(true, kEpiDirect);

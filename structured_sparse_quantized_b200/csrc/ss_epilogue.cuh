@@ -29,11 +29,13 @@ constexpr int kActGeluErf = 4;  // v Phi(v)
 // the registers of the widest, and the TMA ways spill (8192 x 4096 x 4096 with
 // a bias 67 us instead of 64.5).
 constexpr int kEpiNone = 0, kEpiChannels = 1, kEpiTokens = 2, kEpiDirect = 3;
-// kEpiChannels for at most kFewRows tokens: such a product streams the weight,
-// and B tiles this small leave room for a ring of 8 stages instead of 4 (6)
-// (16 tokens, 28672 x 4096 6:8 FP8 gated: 26 -> 22.4 us; weight and selectors 110 MB).
-constexpr int kEpiFew = 4;
+// The TMA ways with tiles of at most kFewRows B rows: such a product streams its
+// A rows, and small B tiles leave room for rings of 5 to 8 stages instead of 2
+// to 6 (16 tokens, 28672 x 4096 6:8 FP8 gated: 26 -> 22.4 us; weight and
+// selectors 110 MB).
+constexpr int kEpiChannelsFew = 4, kEpiTokensFew = 5;
 constexpr int kFewRows = 64;
+constexpr bool epi_is_few(int epi) { return epi == kEpiChannelsFew || epi == kEpiTokensFew; }
 
 struct EpiArgs {
     const void* bias;      // [N], or null
@@ -160,56 +162,6 @@ __device__ __forceinline__ void store_y(void* y, int64_t off, float v) {
         static_cast<__nv_bfloat16*>(y)[off] = __float2bfloat16_rn(v);
     else
         static_cast<float*>(y)[off] = v;
-}
-
-// kN consecutive values at 16-byte aligned memory.
-template <bool kBf16, int kN>
-__device__ __forceinline__ void store_row(void* p, const float (&v)[kN]) {
-    uint4* o = static_cast<uint4*>(p);
-    if constexpr (kBf16) {
-#pragma unroll
-        for (int i = 0; i < kN; i += 8)
-            o[i / 8] = make_uint4(pack_bf16(v[i], v[i + 1]), pack_bf16(v[i + 2], v[i + 3]),
-                                  pack_bf16(v[i + 4], v[i + 5]), pack_bf16(v[i + 6], v[i + 7]));
-    } else {
-#pragma unroll
-        for (int i = 0; i < kN; i += 4)
-            o[i / 4] = make_uint4(__float_as_uint(v[i]), __float_as_uint(v[i + 1]),
-                                  __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3]));
-    }
-}
-
-// v += kN consecutive residual values at 16-byte aligned memory.
-template <int kN>
-__device__ __forceinline__ void add_residual_row(const EpiArgs& e, int64_t off, float (&v)[kN]) {
-    if (e.res_f32) {
-        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(e.residual) + off);
-        float4 u[kN / 4];
-#pragma unroll
-        for (int i = 0; i < kN / 4; ++i) u[i] = p[i];
-#pragma unroll
-        for (int i = 0; i < kN / 4; ++i) {
-            v[4 * i] += u[i].x;
-            v[4 * i + 1] += u[i].y;
-            v[4 * i + 2] += u[i].z;
-            v[4 * i + 3] += u[i].w;
-        }
-    } else {
-        const uint4* p =
-            reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(e.residual) + off);
-        uint4 u[kN / 8];
-#pragma unroll
-        for (int i = 0; i < kN / 8; ++i) u[i] = p[i];
-#pragma unroll
-        for (int i = 0; i < kN / 8; ++i) {
-            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                v[8 * i + 2 * k] += __uint_as_float(w[k] << 16);
-                v[8 * i + 2 * k + 1] += __uint_as_float(w[k] & 0xFFFF0000u);
-            }
-        }
-    }
 }
 
 }  // namespace ss

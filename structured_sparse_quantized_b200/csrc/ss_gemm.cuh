@@ -220,36 +220,53 @@ __device__ __forceinline__ void store_scaled(void* y, int64_t off, uint32_t acc_
         reinterpret_cast<float*>(y)[off] = v;
 }
 
-// Epilogue of one thread's accumulator row (a_row, columns b0 .. b0 + 15)
-// straight to global memory; sa is the row's scale, sb_lane and bias_lane the
-// scale and (token rows) the bias of column b0 + lane % 16, bias_row the bias
-// of a channel row.  read(r) delivers the accumulators; the residual's loads
-// are issued before it, and all of them before the first store.
+// Fused epilogue of a warp's 32 accumulator rows x 16 columns (from b0; this
+// thread's row is a_row) straight to global memory; sa is the row's scale,
+// sb_lane and bias_lane the scale and (token rows) the bias of column b0 + lane
+// % 16, bias_row the bias of a channel row.  read(r) delivers the accumulators;
+// the residual's loads are issued before it, and all of them before the first
+// store.
+//
+// Channel rows: lanes are consecutive outputs, one token per store.  Token rows:
+// a lane's outputs are consecutive, a sector each if they were stored one by one,
+// so the block is turned through the warp's 2 KB of shared memory (columns
+// exchanged by row, which keeps both sides free of bank conflicts) and lanes
+// l, l + 16 store 16 outputs of two tokens (gated: 8 of four).
 template <bool kInt8, bool kOutBf16, typename Read>
-__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, int a_row, int b0, float sa,
-                                                 float sb_lane, float bias_row, float bias_lane,
-                                                 Read read) {
+__device__ __forceinline__ void epi_store_direct(const GemmArgs& args, float* stage, int a_row,
+                                                 int lane, int b0, float sa, float sb_lane,
+                                                 float bias_row, float bias_lane, Read read) {
     const EpiArgs& e = args.epi;
-    const bool row_ok = a_row < args.rowsA;
-    // element u is at off0 + u * stride of Y (and of the residual)
-    const int64_t stride = args.a_is_w ? args.ldy : 1;
-    const int n = row_ok ? min(16, args.rowsB - b0) : 0;
-    // token rows: a thread's 16 (gated: 8) outputs are consecutive, and one by
-    // one they would take a sector each
-    const bool vec = !args.a_is_w && n == 16 && args.ldy % 8 == 0;
-    constexpr int64_t esz = kOutBf16 ? 2 : 4;
+    const bool chan = args.a_is_w != 0;
+    // output i of this thread is at off0 + i * stride, for i < n: channel rows,
+    // (a_row, b0 + i); token rows, the i-th of the turned block
+    int64_t off0, stride;
+    int n, tcol = 0, trow = 0;
+    if (chan) {
+        off0 = static_cast<int64_t>(b0) * args.ldy + (e.gated ? gated_col(a_row) : a_row);
+        stride = args.ldy;
+        n = a_row < args.rowsA && (!e.gated || (a_row & 8) == 0) ? args.rowsB - b0 : 0;
+    } else {
+        const int wide = e.gated ? 3 : 4;  // log2 of the outputs per row of the block
+        trow = lane >> wide;
+        tcol = lane & ((1 << wide) - 1);
+        const int row = a_row - lane + trow, col = (e.gated ? gated_col(b0) : b0) + tcol;
+        off0 = static_cast<int64_t>(row) * args.ldy + col;
+        stride = static_cast<int64_t>(args.ldy) << (5 - wide);
+        const int step = 1 << (5 - wide);
+        n = col < (e.gated ? args.rowsB / 2 : args.rowsB) ? (args.rowsA - row + step - 1) >> (5 - wide)
+                                                          : 0;
+    }
     uint32_t res[16];
-    if (e.residual && !vec) {
-        const int64_t off0 = args.a_is_w ? static_cast<int64_t>(b0) * args.ldy + a_row
-                                         : static_cast<int64_t>(a_row) * args.ldy + b0;
+    if (e.residual) {  // (not gated)
         if (e.res_f32) {
             const uint32_t* p = static_cast<const uint32_t*>(e.residual) + off0;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) res[u] = u < n ? p[u * stride] : 0u;
+            for (int i = 0; i < 16; ++i) res[i] = i < n ? p[i * stride] : 0u;
         } else {
             const uint16_t* p = static_cast<const uint16_t*>(e.residual) + off0;
 #pragma unroll
-            for (int u = 0; u < 16; ++u) res[u] = u < n ? p[u * stride] : 0u;
+            for (int i = 0; i < 16; ++i) res[i] = i < n ? p[i * stride] : 0u;
         }
     }
     uint32_t r[16];
@@ -259,53 +276,47 @@ __device__ __forceinline__ void epi_store_direct(const GemmArgs& args, int a_row
     for (int u = 0; u < 16; ++u) {
         const float sb = __shfl_sync(0xffffffffu, sb_lane, u);
         const float acc = kInt8 ? __int2float_rn(static_cast<int32_t>(r[u])) : __uint_as_float(r[u]);
-        v[u] = args.a_is_w
-                   ? fmaf(__fmul_rn(acc, sb), sa, bias_row)
-                   : fmaf(__fmul_rn(acc, sa), sb, __shfl_sync(0xffffffffu, bias_lane, u));
+        v[u] = chan ? fmaf(__fmul_rn(acc, sb), sa, bias_row)
+                    : fmaf(__fmul_rn(acc, sa), sb, __shfl_sync(0xffffffffu, bias_lane, u));
     }
-    if (!e.gated) {
-        const int64_t off0 = args.a_is_w ? static_cast<int64_t>(b0) * args.ldy + a_row
-                                         : static_cast<int64_t>(a_row) * args.ldy + b0;
-        activate<false>(v, e.act);
-        if (vec) {
-            if (e.residual) add_residual_row<16>(e, off0, v);
-            store_row<kOutBf16, 16>(static_cast<uint8_t*>(args.y) + off0 * esz, v);
-            return;
-        }
-        if (e.residual) {
-            const int shift = e.res_f32 ? 0 : 16;  // bf16: the high half of an fp32
-#pragma unroll
-            for (int u = 0; u < 16; ++u) v[u] += __uint_as_float(res[u] << shift);
-        }
-#pragma unroll
-        for (int u = 0; u < 16; ++u)
-            if (u < n) store_y<kOutBf16>(args.y, off0 + u * stride, v[u]);
-    } else if (args.a_is_w) {  // the partner row is 8 lanes up
+    if (e.gated && chan) {  // the partner row is 8 lanes up
         float up[16];
 #pragma unroll
         for (int u = 0; u < 16; ++u) up[u] = __shfl_down_sync(0xffffffffu, v[u], 8);
         activate<false>(v, e.act);
-        const int64_t off0 = static_cast<int64_t>(b0) * args.ldy + gated_col(a_row);
 #pragma unroll
-        for (int u = 0; u < 16; ++u)
-            if (u < n && (a_row & 8) == 0)
-                store_y<kOutBf16>(args.y, off0 + u * stride, v[u] * up[u]);
-    } else {  // the partner column is this thread's; N is a multiple of 16
+        for (int u = 0; u < 16; ++u) v[u] *= up[u];
+    } else if (e.gated) {  // the partner column is this thread's
         float g[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) g[u] = v[u];
         activate<false>(g, e.act);
-        const int64_t off0 = static_cast<int64_t>(a_row) * args.ldy + gated_col(b0);
+        __syncwarp();  // the block before has been read
 #pragma unroll
-        for (int u = 0; u < 8; ++u) g[u] *= v[u + 8];
-        if (vec) {
-            store_row<kOutBf16, 8>(static_cast<uint8_t*>(args.y) + off0 * esz, g);
-            return;
+        for (int u = 0; u < 8; ++u) stage[lane * 8 + (u ^ (lane >> 2))] = g[u] * v[u + 8];
+        __syncwarp();
+        n = min(n, 8);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = stage[(4 * i + trow) * 8 + (tcol ^ i)];
+    } else {
+        activate<false>(v, e.act);
+        if (!chan) {
+            __syncwarp();
+#pragma unroll
+            for (int u = 0; u < 16; ++u) stage[lane * 16 + (u ^ (lane >> 1))] = v[u];
+            __syncwarp();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = stage[(2 * i + trow) * 16 + (tcol ^ i)];
         }
+        if (e.residual) {
+            const int shift = e.res_f32 ? 0 : 16;  // bf16: the high half of an fp32
 #pragma unroll
-        for (int u = 0; u < 8; ++u)
-            if (u < n) store_y<kOutBf16>(args.y, off0 + u, g[u]);
+            for (int i = 0; i < 16; ++i) v[i] += __uint_as_float(res[i] << shift);
+        }
     }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        if (i < n) store_y<kOutBf16>(args.y, off0 + i * stride, v[i]);
 }
 
 // Output tile t -> (A tile ta, B tile tb).  Consecutive tiles (the ones a
@@ -685,9 +696,10 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
     constexpr bool kFp4 = kQ == kQNvfp4;
     constexpr int kEpiWarps = kEpi ? kFusedEpiWarps : kGemmEpiWarps;
     constexpr int kGroups = kEpiWarps / 4;  // of four epilogue warps
+    constexpr bool kChannels = kEpi == kEpiChannels || kEpi == kEpiChannelsFew;
     using C = std::conditional_t<kFp4, Fp4Cfg<kSparse, kPair, kEpi != kEpiNone>,
                                  GemmCfg<kSparse, kPair, kBf16 ? 2 : 1, kEpi != kEpiNone,
-                                         kEpi == kEpiFew>>;
+                                         epi_is_few(kEpi)>>;
     extern __shared__ __align__(1024) uint8_t smem_dyn[];
     uint8_t* smem = reinterpret_cast<uint8_t*>(
         (reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~static_cast<uintptr_t>(1023));
@@ -1027,7 +1039,7 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
         [[maybe_unused]] auto tile_at = [&](int j) { return unit + j * n_units; };
         if constexpr (kEpi != kEpiNone && kEpi != kEpiDirect) {
             if (args.tma_res && lane == 0)
-                epi_load_residual<kEpi != kEpiTokens>(
+                epi_load_residual<kChannels>(
                     args, walk, epi, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
                     &res_full[ew], n_tiles, tile_at);
         }
@@ -1063,8 +1075,8 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
             const float sa = kFp4 ? __ldg(args.s_a) : load_scale<kBf16>(args.s_a, a_row, row_ok);
             const uint32_t t_row = tmem_base + (static_cast<uint32_t>(q * 32) << 16) +
                                    static_cast<uint32_t>(acc * C::kAccStride);
-            if constexpr (kEpi == kEpiChannels || kEpi == kEpiFew || kEpi == kEpiTokens) {
-                ok = epi_tile_tma<kQ, kEpi != kEpiTokens>(
+            if constexpr (kEpi != kEpiNone && kEpi != kEpiDirect) {
+                ok = epi_tile_tma<kQ, kChannels>(
                     args, walk, epi, tm_y, tm_r, smem + C::kEpiOffset + ew * kFusedWarpBytes,
                     &res_full[ew], abort_flag, n_tiles, a_cta0 + q * 32, b0, lane, t_row, tile_at,
                     [&] {
@@ -1214,7 +1226,9 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
                     for (int half = 0; half < 32; half += 16) {
                         const int from = (lane & 15) + half;
                         epi_store_direct<kInt8, kOutBf16>(
-                            args, a_row, b0 + c + half, sa,
+                            args,
+                            reinterpret_cast<float*>(smem + C::kEpiOffset + ew * kFusedWarpBytes),
+                            a_row, lane, b0 + c + half, sa,
                             __shfl_sync(0xffffffffu, sb_lane, from), bias_row,
                             __shfl_sync(0xffffffffu, bias_col, from), [&](uint32_t (&r)[16]) {
                                 tmem_ld_32x32b_x16(t_row + c + half, r);
