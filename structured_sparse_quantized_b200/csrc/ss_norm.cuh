@@ -334,9 +334,9 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
 // reduction, and a weight read per row costs as much L1 time as the row.
 constexpr int kNormSlots = 4;  // at most: as many as fit shared memory
 
-// 256 threads, or one set of sixteen warps (rows past 8192: eight warps would
-// hold too much of a row each to keep its weights too; 5041 x 13312 78 -> 51 us).
-constexpr int norm_stream_threads(int wpr) { return wpr > 8 ? 32 * wpr : kWarpRowThreads; }
+// As many sets as eight warps hold, or one larger set (rows past 8192: eight warps
+// would hold too much of a row each to keep its weights too; 5041 x 13312 78 -> 51 us).
+constexpr int norm_stream_threads(int wpr) { return 32 * wpr * (wpr > 8 ? 1 : 8 / wpr); }
 
 template <typename T, int kQ, int kChunks, int kWpr>
 __global__ void __launch_bounds__(norm_stream_threads(kWpr)) norm_quant_lift_stream_kernel(

@@ -70,6 +70,8 @@ MANY = [(p, M, K) for M, K in [(1500, 4096), (2500, 264), (4003, 1000), (1300, 2
         for p in ("dense", "4:6", "6:8", "8:10")]
 MANY += [(p, M, K) for M, K in [(1200, 5000), (1190, 6144), (1190, 6136), (1184, 16384), (1190, 8200),
                                 (1184, 13313), (1300, 12304)] for p in ("6:8", "8:10")]
+MANY += [(p, M, K) for M, K in [(1190, 2560), (1185, 7000), (1190, 8192), (1187, 10240), (1190, 14336)]
+         for p in ("dense", "8:10")]
 
 
 @pytest.mark.parametrize("tier", ["int8", "fp8", "bf16"])
