@@ -323,8 +323,12 @@ ss_status ss_dense_gemm_nvfp4_fused(const void *Xv, const void *Xs, const float 
  * (SS_BF16: rounded to bf16 as it is stored).  weight is [K], bf16 or fp32
  * whatever X's type; eps >= 0.  The codes are those of z = X * weight (the
  * row's factor cancels): for bf16 X and weight exactly RNE(Q z / max|z|).
- * Rows must be finite, with a sum of squares below the fp32 range and max|z|
- * below 2^119; a row with max|z| < 1e-35 has codes 0 and s_x 0. */
+ * A row with max|z| < 1e-35 has codes 0 and s_x 0; with eps = 0 the mean of a
+ * row's squares has to be a normal fp32 number.  From max|z| = 2^119 on a code
+ * may be off by a rounding of the quotient.  A row that has no finite norm (NaN
+ * or infinity in X or in z, or a sum of squares past the fp32 range) has s_x
+ * NaN and codes of no meaning (SS_BF16: all of its elements NaN), and thus a
+ * product of NaN; the other rows are as without it. */
 ss_status ss_norm_quant_lift_act(const void *X, ss_in_dtype in_dtype, const void *weight,
                                  ss_in_dtype weight_dtype, float eps, int64_t M, int64_t K,
                                  ss_pattern p, ss_qdtype q, void *Xq_lift, float *s_x,

@@ -760,17 +760,24 @@ __device__ __forceinline__ float relu_nan(float v) {
     return r;
 }
 
-// max(a, |b|, |c|) for a >= 0; NaN operands are passed over.
-__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+// max(a, b); NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
     float r;
-    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
 }
 
-// The largest |v| of the warp's lanes, in every lane.
-__device__ __forceinline__ float warp_max_abs(float v) {
+// max(a, |b|, |c|) for a >= 0; NaN if one of them is.
+__device__ __forceinline__ float max_abs3_nan(float a, float b, float c) {
     float r;
-    asm volatile("redux.sync.max.abs.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// The largest |v| of the warp's lanes, in every lane; NaN if one of them is.
+__device__ __forceinline__ float warp_max_abs_nan(float v) {
+    float r;
+    asm volatile("redux.sync.max.abs.NaN.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
     return r;
 }
 

@@ -12,6 +12,12 @@
 // codes often (1200 of 16M elements at FP8), and they then go to the even code,
 // as the definition says, instead of either way.
 //
+// A row without a finite norm (NaN or infinity in x or in x w, or a sum of squares
+// past the fp32 range) has NaN in s_x, so that all of its product is NaN, as
+// the definition's is for NaN and infinity: the codes alone could not say so in
+// INT8.  In the bf16 tier all of its elements are NaN.  The largest |z| is taken by
+// maxima that keep NaN, which cost what those that pass over it do.
+//
 // The normalised row is never written: X is read and the codes are written,
 // which is all the memory traffic there is.
 #pragma once
@@ -57,9 +63,17 @@ struct NormQuant {
     }
     // s_x of the row with factor r
     __device__ __forceinline__ float scale(float r) const {
-        return hi == 0.0f ? 0.0f : __fdiv_rn(a * r, q_max<kQ == kQInt8>());
+        return a < kNormTiny ? 0.0f : __fdiv_rn(a * r, q_max<kQ == kQInt8>());
     }
 };
+
+// The row's factor, from its sum of squares and largest |z|: NaN unless both are
+// finite.
+__device__ __forceinline__ float norm_factor(float sum, float amax, int K, float eps) {
+    const float top = __int_as_float(0x7F7FFFFF);
+    return sum <= top && amax <= top ? 1.0f / sqrtf(sum / static_cast<float>(K) + eps)
+                                     : __int_as_float(0x7FFFFFFF);
+}
 
 // Four scaled values as four code bytes.
 template <int kQ>
@@ -94,13 +108,13 @@ __device__ __forceinline__ float2 norm_products(float (&z)[kChunks][16], Weight 
             float &z0 = z[i][j], &z1 = z[i][j + 1];
             fma_rn_f32x2(z0, z1, z0, z1, s0, s1, s0, s1);
             mul_rn_f32x2(z0, z1, f[j], f[j + 1], z0, z1);
-            a = max_abs3(a, z0, z1);
+            a = max_abs3_nan(a, z0, z1);
         }
     }
     float s = s0 + s1;
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return make_float2(s, warp_max_abs(a));
+    return make_float2(s, warp_max_abs_nan(a));
 }
 
 // The set's warps' parts together.
@@ -110,7 +124,7 @@ __device__ __forceinline__ float2 norm_combine(const float2 (&part)[kWpr]) {
 #pragma unroll
     for (int i = 1; i < kWpr; ++i) {
         v.x += part[i].x;
-        v.y = fmaxf(v.y, part[i].y);
+        v.y = max_nan(v.y, part[i].y);
     }
     return v;
 }
@@ -129,7 +143,7 @@ __device__ __forceinline__ void norm_write_row(const float (&z)[kChunks][16], fl
     const int Nh = s.Nh, row_bytes = s.K_lp * eb;
     const NormQuant<kQ> nq(sums.y);
     float rn = 0.0f;
-    if (kBf16 || rt == 0) rn = 1.0f / sqrtf(sums.x / static_cast<float>(s.K) + eps);
+    if (kBf16 || rt == 0) rn = norm_factor(sums.x, sums.y, s.K, eps);
     if (!kBf16 && rt == 0) *s_x = nq.scale(rn);
 #pragma unroll
     for (int i = 0; i < kChunks; ++i) {
@@ -458,12 +472,12 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_kernel(
     for (int k = threadIdx.x; k < K; k += kWarpRowThreads) {
         const float f = to_f32<T>(x[k]);
         ss = fmaf(f, f, ss);
-        a = fmaxf(a, fabsf(z_at(k)));
+        a = max_nan(a, fabsf(z_at(k)));
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+        a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, o));
     }
     if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(ss, a);
     __syncthreads();
@@ -471,9 +485,9 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_kernel(
 #pragma unroll
     for (int i = 0; i < kWarpRowThreads / 32; ++i) {
         ss += part[i].x;
-        a = fmaxf(a, part[i].y);
+        a = max_nan(a, part[i].y);
     }
-    const float r = 1.0f / sqrtf(ss / static_cast<float>(K) + eps);
+    const float r = norm_factor(ss, a, K, eps);
     const NormQuant<kQ> nq(a);
     if constexpr (kQ != kQBf16) {
         if (threadIdx.x == 0) s_x[m] = nq.scale(r);
