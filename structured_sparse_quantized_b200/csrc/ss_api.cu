@@ -512,19 +512,28 @@ bool tiles_overflow(int64_t rowsA, int64_t rowsB, int bn) {
     return (rowsA + 127) / 128 * ((rowsB + bn - 1) / bn) > INT32_MAX;
 }
 
-// Opt a row kernel into more than 48 KB of shared memory when needed.  The
+constexpr size_t kMaxRowSmem = 200 * 1024;  // dynamic shared memory of a row kernel, at most
+static_assert(ss::kPruneSmem <= kMaxRowSmem, "every row kernel's calls fit");
+
+// Opts a row kernel into more than 48 KB of shared memory when a call (of `bytes`
+// <= kMaxRowSmem dynamic ones) needs it: once per kernel and device, up to
+// kMaxRowSmem.  One kernel serves calls of many sizes, and the limit belongs to
+// the kernel, not to the call: set to each call's own size, a call on another
+// host thread could lower it between this call's opting in and its launch.  The
 // limit without that counts the kernel's static shared memory too (at most 2 KB
 // in these kernels).
-template <typename Kern>
-ss_status set_smem(Kern kern, int /*dev*/, size_t bytes) {
+template <auto kKern>
+ss_status set_smem(int dev, size_t bytes) {
     if (bytes <= 46 * 1024) return SS_OK;
-    return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                static_cast<int>(bytes)) == cudaSuccess
-               ? SS_OK
-               : SS_ERR_CUDA;
+    static std::once_flag once[kMaxDevices];
+    static cudaError_t err[kMaxDevices];
+    std::call_once(once[dev], [&] {
+        err[dev] = cudaFuncSetAttribute(kKern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                        static_cast<int>(kMaxRowSmem));
+        if (err[dev] != cudaSuccess) cudaGetLastError();
+    });
+    return err[dev] == cudaSuccess ? SS_OK : SS_ERR_CUDA;
 }
-
-constexpr size_t kMaxRowSmem = 200 * 1024;
 
 }  // namespace
 

@@ -75,13 +75,13 @@ int norm_code_row(const ss::NormShape& s, int eb) {
 }
 
 template <typename T, int kQ, int kChunks, int kWpr>
-ss_status launch_norm_reg(const void* X, const void* w, int wf32, float eps, int64_t M,
+ss_status launch_norm_reg(int dev, const void* X, const void* w, int wf32, float eps, int64_t M,
                           const ss::NormShape& shape, void* Xq, float* s_x, cudaStream_t s) {
     constexpr int kSets = ss::kWarpRowThreads / (32 * kWpr);
     const int q_stride = norm_code_row(shape, kQ == ss::kQBf16 ? 2 : 1);
-    auto kern = ss::norm_quant_lift_reg_kernel<T, kQ, kChunks, kWpr>;
+    constexpr auto kern = ss::norm_quant_lift_reg_kernel<T, kQ, kChunks, kWpr>;
     const size_t smem = static_cast<size_t>(kSets) * q_stride;
-    const ss_status st = set_smem(kern, 0, smem);
+    const ss_status st = set_smem<kern>(dev, smem);
     if (st != SS_OK) return st;
     return launch_ex(kern, dim3(static_cast<unsigned>((M + kSets - 1) / kSets)),
                      dim3(ss::kWarpRowThreads), smem, s, 1, static_cast<const T*>(X), w, wf32, eps,
@@ -95,11 +95,11 @@ ss_status launch_norm_stream(int dev, const void* X, const void* w, int wf32, fl
     constexpr int64_t kSets = kThreads / (32 * kWpr);
     const int q_stride = norm_code_row(shape, kQ == ss::kQBf16 ? 2 : 1);
     const int slot = static_cast<int>(round_up(shape.K * static_cast<int64_t>(sizeof(T)), 128));
-    auto kern = ss::norm_quant_lift_stream_kernel<T, kQ, kChunks, kWpr>;
+    constexpr auto kern = ss::norm_quant_lift_stream_kernel<T, kQ, kChunks, kWpr>;
     const int n_slots = static_cast<int>(std::min<int64_t>(
         ss::kNormSlots, (static_cast<int64_t>(kMaxRowSmem) / kSets - q_stride) / slot));
     const size_t smem = static_cast<size_t>(kSets) * (n_slots * slot + q_stride);
-    const ss_status st = set_smem(kern, dev, smem);
+    const ss_status st = set_smem<kern>(dev, smem);
     if (st != SS_OK) return st;
     int per_sm = 0;
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kThreads, smem) !=
@@ -119,7 +119,8 @@ ss_status launch_norm(int dev, const void* X, const void* w, int wf32, float eps
                       cudaStream_t s) {
     const ss::NormShape shape = {static_cast<int>(K), Nh, static_cast<int>(K_lift),
                                  static_cast<int>(K_lp), static_cast<int>((K + 15) / 16)};
-#define SS_NORM_REG(C, W) return launch_norm_reg<T, kQ, C, W>(X, w, wf32, eps, M, shape, Xq, s_x, s)
+#define SS_NORM_REG(C, W) \
+    return launch_norm_reg<T, kQ, C, W>(dev, X, w, wf32, eps, M, shape, Xq, s_x, s)
 #define SS_NORM_STREAM(C, W) \
     return launch_norm_stream<T, kQ, C, W>(dev, X, w, wf32, eps, M, shape, Xq, s_x, s)
     const bool stream = K * static_cast<int64_t>(sizeof(T)) % 16 == 0 &&

@@ -36,8 +36,8 @@ ss_status ss_compress_weight(const void* W, ss_in_dtype in_dtype, int64_t N, int
     const int64_t rows_grid = dense ? N : (N + 127) / 128 * 128;
 #define SS_COMPRESS(T, Q)                                                                      \
     do {                                                                                      \
-        auto kern = ss::compress_weight_kernel<T, Q>;                                         \
-        if ((st = set_smem(kern, dev, smem)) != SS_OK) return st;                             \
+        constexpr auto kern = ss::compress_weight_kernel<T, Q>;                               \
+        if ((st = set_smem<kern>(dev, smem)) != SS_OK) return st;                             \
         st = launch_ex(kern, dim3(static_cast<unsigned>(rows_grid)), dim3(ss::kCompressThreads), \
                        smem, s, 1, static_cast<const T*>(W), N, K, p.keep, p.group, K_lift,   \
                        K_lp, wv, wm, s_w);                                                    \
@@ -102,8 +102,8 @@ ss_status ss_quant_lift_act(const void* X, ss_in_dtype in_dtype, int64_t M, int6
     const unsigned grid = static_cast<unsigned>((M + warps - 1) / warps);
 #define SS_QLIFT(T, I8)                                                                        \
     do {                                                                                      \
-        auto kern = ss::quant_lift_warp_kernel<T, I8>;                                        \
-        if ((st = set_smem(kern, dev, smem)) != SS_OK) return st;                             \
+        constexpr auto kern = ss::quant_lift_warp_kernel<T, I8>;                              \
+        if ((st = set_smem<kern>(dev, smem)) != SS_OK) return st;                             \
         st = launch_ex(kern, dim3(grid), dim3(warps * 32), smem, s, 1,                        \
                        static_cast<const T*>(X), M, K, Nh, K_lift, K_lp, q_stride, xq, s_x);  \
     } while (0)
@@ -121,8 +121,8 @@ ss_status ss_quant_lift_act(const void* X, ss_in_dtype in_dtype, int64_t M, int6
         const size_t rsmem = Nh == 4 ? 0 : static_cast<size_t>(rows_per_cta) * q_stride;
 #define SS_QREG(I8, C, W)                                                                      \
     do {                                                                                      \
-        auto kern = ss::quant_lift_reg_kernel<I8, C, W>;                                      \
-        if ((st = set_smem(kern, dev, rsmem)) != SS_OK) return st;                            \
+        constexpr auto kern = ss::quant_lift_reg_kernel<I8, C, W>;                            \
+        if ((st = set_smem<kern>(dev, rsmem)) != SS_OK) return st;                            \
         st = launch_ex(kern, dim3(rgrid), dim3(ss::kWarpRowThreads), rsmem, s, 1, xb, M, K,   \
                        Nh, K_lift, K_lp, q_stride, xq, s_x);                                 \
     } while (0)
@@ -199,8 +199,8 @@ ss_status ss_prune_act_2to4(const void* X, ss_in_dtype in_dtype, int64_t M, int6
         const int Mi = static_cast<int>(M), Ki = static_cast<int>(K), Kl = static_cast<int>(K_lp);
 #define SS_PRUNE_ST(Q, S, W, F)                                                               \
     do {                                                                                      \
-        auto kern = ss::prune_act_stream_kernel<Q, S, W, F>;                                  \
-        if ((st = set_smem(kern, dev, ss::kPruneSmem)) != SS_OK) return st;                   \
+        constexpr auto kern = ss::prune_act_stream_kernel<Q, S, W, F>;                        \
+        if ((st = set_smem<kern>(dev, ss::kPruneSmem)) != SS_OK) return st;                   \
         return launch_ex(kern, dim3(pgrid), dim3(ss::kWarpRowThreads), ss::kPruneSmem, s, 1,  \
                          xb, Mi, Ki, Kl, xv, xm, s_x, 1u);                                    \
     } while (0)
@@ -278,10 +278,10 @@ ss_status ss_compress_weight_nvfp4(const void* W, ss_in_dtype in_dtype, int64_t 
     auto* ws = static_cast<uint8_t*>(Ws);
 #define SS_FP4W(T)                                                                             \
     do {                                                                                      \
-        auto k1 = ss::fp4_weight_amax_kernel<T>;                                               \
-        auto k2 = ss::compress_weight_nvfp4_kernel<T>;                                         \
-        if ((st = set_smem(k1, dev, smem1)) != SS_OK) return st;                              \
-        if ((st = set_smem(k2, dev, smem2)) != SS_OK) return st;                              \
+        constexpr auto k1 = ss::fp4_weight_amax_kernel<T>;                                    \
+        constexpr auto k2 = ss::compress_weight_nvfp4_kernel<T>;                              \
+        if ((st = set_smem<k1>(dev, smem1)) != SS_OK) return st;                              \
+        if ((st = set_smem<k2>(dev, smem2)) != SS_OK) return st;                              \
         const T* w = static_cast<const T*>(W);                                                \
         if ((st = launch_ex(k1, dim3(static_cast<unsigned>(N)), dim3(ss::kCompressThreads),   \
                             smem1, s, 1, w, N, K, p.keep, p.group, amax)) != SS_OK)           \
