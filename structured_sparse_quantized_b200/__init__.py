@@ -293,14 +293,31 @@ def ss_debug_skip_stage(kb: int) -> None:
 
 # ------------------------------------------------------------------ allocating wrappers
 # Stored values are uint8 codes for the 8-bit tiers and bfloat16 for the bf16
-# tier, which has no scales (its s_* entries are None).
+# tier, which has no scales (its s_* entries are None).  What a call allocates,
+# outputs and intermediates, is allocated for the stream that it runs on.
 
 def _vals_dtype(q) -> torch.dtype:
     return torch.bfloat16 if _qdtype(q) == SS_BF16 else torch.uint8
 
 
-def _scales(n: int, q, dev):
-    return None if _qdtype(q) == SS_BF16 else torch.empty(n, dtype=torch.float32, device=dev)
+def _new(like: torch.Tensor, shape, dtype, stream):
+    """A tensor on like's device, allocated for the stream that will write it (so
+    that its memory is reused in that stream's order)."""
+    if stream is None or not like.is_cuda:
+        return like.new_empty(shape, dtype=dtype)
+    with _as_current(stream, like):
+        return like.new_empty(shape, dtype=dtype)
+
+
+def _as_current(stream, like: torch.Tensor):
+    """Context in which `stream` (a Stream or a handle) is the current one."""
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
+    return torch.cuda.stream(stream)
+
+
+def _scales(like: torch.Tensor, n: int, q, stream):
+    return None if _qdtype(q) == SS_BF16 else _new(like, (n,), torch.float32, stream)
 
 
 def compress_weight(W: torch.Tensor, pattern, q, stream=None):
@@ -308,15 +325,14 @@ def compress_weight(W: torch.Tensor, pattern, q, stream=None):
     N, K = W.shape
     p = _pattern(pattern)
     _, _, K_lp = ss_slide_shape(p, K)
-    dev = W.device
     vd = _vals_dtype(q)
     if p.group == 0:
-        Wv = torch.empty((N, K_lp), dtype=vd, device=dev)
+        Wv = _new(W, (N, K_lp), vd, stream)
         Wm = None
     else:
-        Wv = torch.empty((N, K_lp // 2), dtype=vd, device=dev)
-        Wm = torch.empty(meta_shape(N, K_lp), dtype=torch.uint8, device=dev)
-    s_w = _scales(N, q, dev)
+        Wv = _new(W, (N, K_lp // 2), vd, stream)
+        Wm = _new(W, meta_shape(N, K_lp), torch.uint8, stream)
+    s_w = _scales(W, N, q, stream)
     ss_compress_weight(W, p, q, Wv, Wm, s_w, stream)
     return Wv, Wm, s_w
 
@@ -326,8 +342,7 @@ def quant_lift_act(X: torch.Tensor, pattern, q, stream=None, out=None):
     p = _pattern(pattern)
     _, _, K_lp = ss_slide_shape(p, K)
     if out is None:
-        out = (torch.empty((M, K_lp), dtype=_vals_dtype(q), device=X.device),
-               _scales(M, q, X.device))
+        out = (_new(X, (M, K_lp), _vals_dtype(q), stream), _scales(X, M, q, stream))
     ss_quant_lift_act(X, p, q, out[0], out[1], stream)
     return out
 
@@ -336,9 +351,8 @@ def prune_act_2to4(X: torch.Tensor, q, stream=None, out=None):
     M, K = X.shape
     K_lp = ss_act_2to4_shape(K)
     if out is None:
-        out = (torch.empty((M, K_lp // 2), dtype=_vals_dtype(q), device=X.device),
-               torch.empty(meta_shape(M, K_lp), dtype=torch.uint8, device=X.device),
-               _scales(M, q, X.device))
+        out = (_new(X, (M, K_lp // 2), _vals_dtype(q), stream),
+               _new(X, meta_shape(M, K_lp), torch.uint8, stream), _scales(X, M, q, stream))
     ss_prune_act_2to4(X, q, out[0], out[1], out[2], stream)
     return out
 
@@ -352,7 +366,7 @@ def sparse_gemm(sparse_operand: int, Av, Am, s_a, B, s_b, M: int, N: int, q,
                              stream)
         return out
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=Av.device)
+        out = _new(Av, (M, N), out_dtype, stream)
     ss_sparse_gemm(sparse_operand, Av, Am, s_a, B, s_b, M, N, K_lp, q, out, stream)
     return out
 
@@ -366,7 +380,7 @@ def dense_gemm(Xq, s_x, Wq, s_w, q, out_dtype=torch.bfloat16, stream=None, out=N
         ss_dense_gemm_fused(Xq, s_x, Wq, s_w, M, N, K_p, q, epilogue, out, stream)
         return out
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=Xq.device)
+        out = _new(Xq, (M, N), out_dtype, stream)
     ss_dense_gemm(Xq, s_x, Wq, s_w, M, N, K_p, q, out, stream)
     return out
 
@@ -377,7 +391,8 @@ def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream
     GEMM (or the dense GEMM for pattern 'dense').  `packed` = compress_weight().
     norm = (weight, eps): RMS norm of X fused into the quantisation.
     epilogue: bias, activation and residual fused into the GEMM."""
-    if stream is not None and (epilogue is not None or norm is not None):
+    _index(X, "X")
+    if stream is not None:
         with _as_current(stream, X):  # the quantised activation is that stream's too
             return linear(X, packed, pattern, q, out_dtype, None, epilogue, norm, out)
     Wv, Wm, s_w = packed
@@ -446,16 +461,15 @@ def compress_weight_nvfp4(W: torch.Tensor, pattern, stream=None):
     N, K = W.shape
     p = _pattern(pattern)
     _, K_lp = ss_fp4_shape(p, K)
-    dev = W.device
     if p.group == 0:
-        Wv = torch.empty((N, K_lp // 2), dtype=torch.uint8, device=dev)
+        Wv = _new(W, (N, K_lp // 2), torch.uint8, stream)
         Wm = None
-        Ws = torch.empty(ss_fp4_scale_bytes(N, K_lp, 16), dtype=torch.uint8, device=dev)
+        Ws = _new(W, (ss_fp4_scale_bytes(N, K_lp, 16),), torch.uint8, stream)
     else:
-        Wv = torch.empty((N, K_lp // 4), dtype=torch.uint8, device=dev)
-        Wm = torch.empty(meta_shape(N, K_lp // 2), dtype=torch.uint8, device=dev)
-        Ws = torch.empty(ss_fp4_scale_bytes(N, K_lp, 32), dtype=torch.uint8, device=dev)
-    g_w = torch.empty(4, dtype=torch.float32, device=dev)   # [0] is the global scale
+        Wv = _new(W, (N, K_lp // 4), torch.uint8, stream)
+        Wm = _new(W, meta_shape(N, K_lp // 2), torch.uint8, stream)
+        Ws = _new(W, (ss_fp4_scale_bytes(N, K_lp, 32),), torch.uint8, stream)
+    g_w = _new(W, (4,), torch.float32, stream)   # [0] is the global scale
     ss_compress_weight_nvfp4(W, p, Wv, Wm, Ws, g_w, stream)
     return Wv, Wm, Ws, g_w
 
@@ -466,9 +480,9 @@ def quant_lift_act_nvfp4(X: torch.Tensor, pattern, block: int, stream=None, out=
     p = _pattern(pattern)
     _, K_lp = ss_fp4_shape(p, K)
     if out is None:
-        out = (torch.empty((M, K_lp // 2), dtype=torch.uint8, device=X.device),
-               torch.empty(ss_fp4_scale_bytes(M, K_lp, block), dtype=torch.uint8, device=X.device),
-               torch.empty(4, dtype=torch.float32, device=X.device))
+        out = (_new(X, (M, K_lp // 2), torch.uint8, stream),
+               _new(X, (ss_fp4_scale_bytes(M, K_lp, block),), torch.uint8, stream),
+               _new(X, (4,), torch.float32, stream))
     ss_quant_lift_act_nvfp4(X, p, block, out[0], out[1], out[2], stream)
     return out
 
@@ -484,7 +498,7 @@ def sparse_gemm_nvfp4(packed, act, M: int, N: int, out_dtype=torch.bfloat16, str
                                    stream)
         return out
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=Xv.device)
+        out = _new(Xv, (M, N), out_dtype, stream)
     ss_sparse_gemm_nvfp4(Wv, Wm, Ws, g_w, Xv, Xs, g_x, M, N, K_lp, out, stream)
     return out
 
@@ -499,7 +513,7 @@ def dense_gemm_nvfp4(act, packed, M: int, N: int, out_dtype=torch.bfloat16, stre
         ss_dense_gemm_nvfp4_fused(Xv, Xs, g_x, Wv, Ws, g_w, M, N, K_p, epilogue, out, stream)
         return out
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype, device=Xv.device)
+        out = _new(Xv, (M, N), out_dtype, stream)
     ss_dense_gemm_nvfp4(Xv, Xs, g_x, Wv, Ws, g_w, M, N, K_p, out, stream)
     return out
 
@@ -509,7 +523,8 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
     """Y = X W^T in NVFP4: quantisation with one global scale for X + pair
     lift (blocks of 32 for a sparse weight, 16 for a dense one), then the
     block-scaled GEMM, with the fused epilogue if one is given."""
-    if stream is not None and epilogue is not None:
+    _index(X, "X")
+    if stream is not None:
         with _as_current(stream, X):
             return linear_nvfp4(X, packed, pattern, out_dtype, None, epilogue, out)
     dense = _pattern(pattern).group == 0
@@ -541,22 +556,6 @@ def _raw_stream(stream, index: int) -> int:
     if stream is None:
         return torch._C._cuda_getCurrentRawStream(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-
-
-def _new(like: torch.Tensor, shape, dtype, stream):
-    """A tensor on like's device, allocated for the stream that will write it (so
-    that its memory is reused in that stream's order)."""
-    if stream is None:
-        return like.new_empty(shape, dtype=dtype)
-    with _as_current(stream, like):
-        return like.new_empty(shape, dtype=dtype)
-
-
-def _as_current(stream, like: torch.Tensor):
-    """Context in which `stream` (a Stream or a handle) is the current one."""
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device)
-    return torch.cuda.stream(stream)
 
 
 def _index(t, name: str) -> int:
