@@ -390,19 +390,22 @@ def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream
     """Y = X W^T through the weight-sparse path: quant+lift, then the sparse
     GEMM (or the dense GEMM for pattern 'dense').  `packed` = compress_weight().
     norm = (weight, eps): RMS norm of X fused into the quantisation.
-    epilogue: bias, activation and residual fused into the GEMM."""
+    epilogue: bias, activation and residual fused into the GEMM.
+    out: the [M, N] output (a gated one [M, N/2])."""
     _index(X, "X")
     if stream is not None:
         with _as_current(stream, X):  # the quantised activation is that stream's too
             return linear(X, packed, pattern, q, out_dtype, None, epilogue, norm, out)
     Wv, Wm, s_w = packed
-    M = X.shape[0]
+    M, K = X.shape
     N = Wv.shape[0]
+    p, K_lp = _pattern_k_lp(pattern, K)
+    _fits(M, N, K, K_lp, Wv.shape[1] * (1 if p.group == 0 else 2), out, epilogue)
     if norm is None:
         Xq, s_x = quant_lift_act(X, pattern, q, stream)
     else:
         Xq, s_x = norm_quant_lift_act(X, norm[0], norm[1], pattern, q, stream)
-    if _pattern(pattern).group == 0:
+    if p.group == 0:
         return dense_gemm(Xq, s_x, Wv, s_w, q, out_dtype, stream, out, epilogue)
     return sparse_gemm(0, Wv, Wm, s_w, Xq, s_x, M, N, q, out_dtype, stream, out, epilogue)
 
@@ -522,14 +525,18 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
                  epilogue=None, out=None):
     """Y = X W^T in NVFP4: quantisation with one global scale for X + pair
     lift (blocks of 32 for a sparse weight, 16 for a dense one), then the
-    block-scaled GEMM, with the fused epilogue if one is given."""
+    block-scaled GEMM, with the fused epilogue if one is given.  out: the
+    [M, N] output (a gated one [M, N/2])."""
     _index(X, "X")
     if stream is not None:
         with _as_current(stream, X):
             return linear_nvfp4(X, packed, pattern, out_dtype, None, epilogue, out)
-    dense = _pattern(pattern).group == 0
-    act = quant_lift_act_nvfp4(X, pattern, 16 if dense else 32, stream)
-    M, N = X.shape[0], packed[0].shape[0]
+    p = _pattern(pattern)
+    dense = p.group == 0
+    (M, K), N = X.shape, packed[0].shape[0]
+    _fits(M, N, K, _fp4_k_lp(p.keep, p.group, K), packed[0].shape[1] * (2 if dense else 4), out,
+          epilogue)
+    act = quant_lift_act_nvfp4(X, p, 16 if dense else 32, stream)
     if dense:
         return dense_gemm_nvfp4(act, packed, M, N, out_dtype, stream, out, epilogue)
     return sparse_gemm_nvfp4(packed, act, M, N, out_dtype, stream, out, epilogue)
@@ -604,6 +611,21 @@ def _pattern_named(s: str) -> ss_pattern:
 @functools.lru_cache(maxsize=4096)
 def _k_lp(keep: int, group: int, K: int) -> int:
     return ss_slide_shape(_pattern_of(keep, group), K)[2]
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp4_k_lp(keep: int, group: int, K: int) -> int:
+    return ss_fp4_shape(_pattern_of(keep, group), K)[1]
+
+
+def _fits(M, N, K, K_lp, weight_k_lp, out, epilogue) -> None:
+    """An activation [M, K] (K_lp lifted) and an output, if one is given, against
+    a weight of N rows of weight_k_lp: the products themselves take pointers."""
+    if K_lp != weight_k_lp:
+        raise ValueError(f"X has {K} columns, {K_lp} lifted; the weight has {weight_k_lp}")
+    shape = (M, N // 2 if epilogue is not None and epilogue.gated else N)
+    if out is not None and out.shape != shape:
+        raise ValueError(f"out must have shape {shape}, got {tuple(out.shape)}")
 
 
 def _pattern_k_lp(pattern, K: int):
