@@ -316,6 +316,15 @@ def _as_current(stream, like: torch.Tensor):
     return torch.cuda.stream(stream)
 
 
+def _away(X: torch.Tensor, stream):
+    """Context in which `stream`, or else X's device, is the current one; None
+    where it is already."""
+    d = _index(X, "X")
+    if stream is not None:
+        return _as_current(stream, X)
+    return None if torch._C._cuda_getDevice() == d else torch.cuda.device(d)
+
+
 def _scales(like: torch.Tensor, n: int, q, stream):
     return None if _qdtype(q) == SS_BF16 else _new(like, (n,), torch.float32, stream)
 
@@ -392,9 +401,9 @@ def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream
     norm = (weight, eps): RMS norm of X fused into the quantisation.
     epilogue: bias, activation and residual fused into the GEMM.
     out: the [M, N] output (a gated one [M, N/2])."""
-    _index(X, "X")
-    if stream is not None:
-        with _as_current(stream, X):  # the quantised activation is that stream's too
+    away = _away(X, stream)
+    if away:
+        with away:  # the quantised activation is that stream's too
             return linear(X, packed, pattern, q, out_dtype, None, epilogue, norm, out)
     Wv, Wm, s_w = packed
     M, K = X.shape
@@ -527,9 +536,9 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
     lift (blocks of 32 for a sparse weight, 16 for a dense one), then the
     block-scaled GEMM, with the fused epilogue if one is given.  out: the
     [M, N] output (a gated one [M, N/2])."""
-    _index(X, "X")
-    if stream is not None:
-        with _as_current(stream, X):
+    away = _away(X, stream)
+    if away:
+        with away:
             return linear_nvfp4(X, packed, pattern, out_dtype, None, epilogue, out)
     p = _pattern(pattern)
     dense = p.group == 0
@@ -544,8 +553,8 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
 
 # ------------------------------------------------------------------ fused epilogue
 # The calls below check shapes, types and devices (ValueError) before the C
-# call, and run on the device of their tensors, on its current stream, whatever
-# device is current.
+# call; they, linear and linear_nvfp4 run on the device of their tensors, on its
+# current stream, whatever device is current.
 
 def _call(where: str, index: int, *args) -> None:
     """The C function `where`, with device `index` current."""
