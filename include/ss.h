@@ -187,6 +187,8 @@ ss_status ss_dense_gemm(const void *Xq, const float *s_x, const void *Wq, const 
  *   SS_ACT_SILU      v / (1 + e^-v)
  *   SS_ACT_GELU      v (1 + tanh(sqrt(2/pi) (v + 0.044715 v^3))) / 2
  *   SS_ACT_GELU_ERF  v (1 + erf(v / sqrt 2)) / 2
+ * At v = -inf SILU and GELU are NaN, as these formulas are, RELU and GELU_ERF
+ * are 0.  Results of act below 88 * 2^-126 in magnitude may come out as 0.
  * bias is [N], residual [M, N] row-major, each NULL or 16-byte aligned, bf16
  * or fp32 whatever Y's type.  The residual may be Y itself (same type): it is
  * then updated in place; otherwise Y overlaps no input.  SS_ERR_INVALID_ARG:
