@@ -195,7 +195,7 @@ struct GemmArgs {
     int a_is_w;       // 1: A rows are output channels (Y[b, a]); 0: Y[a, b]
     int ldy;          // leading dimension of Y (= N)
     int tma_res;      // 1: the residual is bf16 and comes by TMA through the staging
-                      //    buffers (kEpi, with tma_store and a_is_w)
+                      //    buffers (kEpi, with tma_store)
     int tma_store;    // 1: Y written by TMA tensor stores through shared memory
                       //    (A rows = channels: 128B-swizzled [32][64] halves)
     int e_chunks;     // K_lp / 128: 2 KB metadata tiles per 128 rows (tile-major)
@@ -1020,6 +1020,9 @@ __global__ void __launch_bounds__(kEpi ? kFusedThreads : kGemmThreads, 1)
         // keeps the epilogue shorter than the MMAs of a tile when K is short.
         // Without TMA stores (fp32 Y, or Y rows not 16-byte aligned) the
         // values go straight to global memory.
+        // With the fused epilogue four groups take the chunks g, g + 4, ..., and
+        // each warp has a staging buffer, stores and waits of its own
+        // (epi_tile_tma, epi_store_direct): nothing is shared in a group.
         const int ew = warp - 2;
         const int grp = ew >> 2;  // chunk parity of this group
         const uint32_t grp_bar = 1 + static_cast<uint32_t>(grp);

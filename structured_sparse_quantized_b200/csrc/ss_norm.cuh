@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kWarpRowThreads) norm_quant_lift_reg_kernel(
 // the weights of its chunks in registers and kNormSlots rows in flight from
 // HBM into shared memory (1-D bulk copies), so that the copies of the next
 // rows go on while a row is reduced, quantised and stored.  Bound by HBM: 16384
-// rows of 4096 bf16 to 6:8 FP8 in 44 us, 83% of the measured copy rate.
+// rows of 4096 bf16 to 6:8 FP8 in 44-47 us, 78-83% of the measured copy rate.
 // Without the copies in flight (rows straight to registers, 2 to 8 warps per
 // row) 16384 rows of 4096 took 50-89 us: the loads pause in every row's
 // reduction, and a weight read per row costs as much L1 time as the row.
