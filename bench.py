@@ -59,13 +59,13 @@ IDEAL = {"2:4": 2.0, "4:6": 1.5, "6:8": 4.0 / 3.0, "8:10": 1.25}
 # device code and the host code that picks its shape) and their hash at
 # capture time (csrc_hash).  A stored figure is reported only while those
 # sources still hash the same; otherwise "traffic" is null.
-GEMM_SOURCES = ("ss_api.cu", "ss_common.cuh", "ss_gemm.cuh", "ss_gemm_wide.cuh")
+GEMM_SOURCES = ("ss_api.cu", "ss_common.cuh", "ss_epilogue.cuh", "ss_gemm.cuh", "ss_gemm_wide.cuh")
 TRAFFIC = {
     ("llama_layer_gate_up", 16384, "6:8", "int8"): {
-        "bytes": (293.88e6 + 430.32e6 + 293.93e6 + 427.31e6) / 2,
+        "bytes": (291.63e6 + 430.83e6 + 291.73e6 + 427.59e6) / 2,
         "profile": "profiles/gemm_llama_gateup_6of8_int8_m16384.md",
         "sources": GEMM_SOURCES,
-        "csrc_hash": "c1d5dfba79d74249"},
+        "csrc_hash": "19329f4daf03e454"},
 }
 
 
