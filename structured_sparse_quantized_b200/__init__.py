@@ -897,7 +897,8 @@ def feed_forward(X: torch.Tensor, packed_gate_up, packed_down, pattern, q, act="
                  stream=None):
     """The feed-forward half of a transformer layer, X + down(act(gate) * up)
     with gate, up of the RMS norm of X (norm = (weight, eps) or None):
-    `packed_gate_up` = compress_weight(interleave_gate_up(W_gate, W_up)).
+    `packed_gate_up` = compress_weight(interleave_gate_up(W_gate, W_up)).  What
+    the down projection takes is rounded to bf16 first, whatever X's type.
     -> [M, K] of X's type."""
     if stream is not None:
         with _as_current(stream, X):
