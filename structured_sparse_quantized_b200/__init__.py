@@ -402,7 +402,7 @@ def linear(X: torch.Tensor, packed, pattern, q, out_dtype=torch.bfloat16, stream
     epilogue: bias, activation and residual fused into the GEMM.
     out: the [M, N] output (a gated one [M, N/2])."""
     away = _away(X, stream)
-    if away:
+    if away is not None:
         with away:  # the quantised activation is that stream's too
             return linear(X, packed, pattern, q, out_dtype, None, epilogue, norm, out)
     Wv, Wm, s_w = packed
@@ -537,7 +537,7 @@ def linear_nvfp4(X: torch.Tensor, packed, pattern, out_dtype=torch.bfloat16, str
     block-scaled GEMM, with the fused epilogue if one is given.  out: the
     [M, N] output (a gated one [M, N/2])."""
     away = _away(X, stream)
-    if away:
+    if away is not None:
         with away:
             return linear_nvfp4(X, packed, pattern, out_dtype, None, epilogue, out)
     p = _pattern(pattern)
